@@ -75,7 +75,9 @@ enum {
   KVSEL_ERR_NONFINITE = 3,    /* device: a window logit was NaN or +-Inf */
   KVSEL_ERR_TIMEOUT = 4,      /* device: a bounded wait ran out */
   KVSEL_ERR_CUDA = 5,         /* a CUDA runtime call failed */
-  KVSEL_ERR_BAD_INDEX = 6     /* device: a gather index was outside [0, L_b) */
+  KVSEL_ERR_BAD_INDEX = 6,    /* device: an index, page number or length was out of range */
+  KVSEL_ERR_NO_PAGES = 7,     /* device: the pool had too few free pages */
+  KVSEL_ERR_SHARED_PAGE = 8   /* device: a page to be rewritten is held by several sequences */
 };
 
 enum { KVSEL_POOL_AVG = 0, KVSEL_POOL_MAX = 1 };
@@ -337,6 +339,193 @@ kvsel_status kvsel_decode_quality(int64_t n, int32_t D, const float* lse_keep,
  * C < 1, g < 0 or NULL arrays (num_seqs > 0). */
 kvsel_status kvsel_cache_lengths(const kvsel_shape* shape, int32_t C, int32_t g,
                                  int64_t* physical_length, int64_t* next_logical);
+
+/* ---------------------------------------------------------------------------
+ * Paged caches. A server keeps its sequences' caches in pages of a pool; a
+ * cache that kvsel_snapkv or kvsel_select has cut is read, grown, cut again
+ * and shared there with the four calls below. They take every length, table
+ * and index from device memory, allocate nothing and copy nothing from the
+ * host, so one captured graph serves steps whose lengths differ; their scratch
+ * is the caller's `workspace` (two calls that may overlap on the GPU, or two
+ * graphs that may replay at once, need one each; it needs no initial value).
+ * Make the first call on a device before a stream capture (it looks up the
+ * status word's address).
+ *
+ * Pool: K and V [num_layers][num_pages][page_size][H_kv][D], K and V with the
+ * same strides. layer_stride and page_stride are in elements, 0 = dense (the
+ * layout above); others allow for a pool that interleaves layers or K and V,
+ * for instance. Table: [num_seqs][table_width] int32 page numbers, one table for
+ * every layer; row j of sequence b (its physical slot, see kvsel_cache_lengths)
+ * is row j % page_size of page table[b][j / page_size]. Lengths: int32 rows per
+ * sequence, 0 allowed. Only the entries that the lengths reach are read.
+ * Rules of every call: INVALID_ARG for a NULL or broken descriptor (counts < 1,
+ * num_pages < 0, a stride below a page's elements), NULL pointers where data is
+ * needed, K or V or a stride not 32-byte aligned; UNSUPPORTED for D not in
+ * {64, 128}, a page_size that is no power of two, a pool of 2^31 or more rows or
+ * 128 GiB or more per layer, a table of 2^31 or more rows per sequence. A packed
+ * cache [num_layers][T][H_kv][D] is a pool of T pages of one row.
+ * ------------------------------------------------------------------------- */
+typedef struct kvsel_pages {
+  int32_t num_layers;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+  int64_t layer_stride; /* elements, 0 = dense */
+  int64_t page_stride;  /* elements, 0 = dense */
+  void* K;
+  void* V;
+} kvsel_pages;
+
+/* Rows of new tokens: token n of layer l is `heads` x D contiguous elements at
+ * data + l * layer_stride + n * token_stride (elements; each row 16-byte
+ * aligned), so q, k and v may be slices of one fused projection. */
+typedef struct kvsel_rows {
+  const void* data;
+  int64_t layer_stride;
+  int64_t token_stride;
+} kvsel_rows;
+
+/* Position rotation of the first rot_dim elements of a head. Pair i < rot_dim/2
+ * turns by the angle position * inv_freq[i] (device, fp32; the angle is off by less
+ * than 2^-20 + |position * inv_freq[i]| 2^-43 rad): elements (i, i + rot_dim/2), or
+ * (2i, 2i + 1) when interleaved; both results are multiplied by `scale`.
+ * rot_dim 0: no rotation. kvsel_rope_frequencies fills inv_freq and scale. */
+typedef struct kvsel_rope {
+  int32_t rot_dim;
+  int32_t interleaved;
+  const float* inv_freq;
+  float scale;
+} kvsel_rope;
+
+enum {
+  KVSEL_ROPE_PLAIN = 0,  /* inv_freq[i] = base^(-2i/rot_dim) */
+  KVSEL_ROPE_LINEAR = 1, /* all divided by factor */
+  KVSEL_ROPE_BASE = 2,   /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+  KVSEL_ROPE_PARTS = 3   /* pairs of fewer than `low` turns over original_len rows divided by
+                            factor, of more than `high` left, in between interpolated linearly
+                            in the number of turns; scale = 1 + 0.1 ln(factor) */
+};
+
+/* Host only: inv_freq[rot_dim / 2] (HOST array, computed in fp64, rounded once)
+ * and *scale (1 but for PARTS) for a context `factor` times as long as the
+ * `original_len` rows that a model was made for. INVALID_ARG for rot_dim < 2 or
+ * odd, base <= 1, factor < 1, an unknown kind, NULL pointers; for BASE with
+ * rot_dim 2; for PARTS with original_len < 1 or not 0 < low < high. */
+kvsel_status kvsel_rope_frequencies(int32_t rot_dim, double base, int32_t kind, double factor,
+                                    int64_t original_len, double low, double high,
+                                    float* inv_freq, float* scale);
+
+/* New tokens into a paged cache, in one pass: the norm of every query and key
+ * head, x * rsqrt(mean(x^2) + eps) * weight (q_weight, k_weight
+ * [num_layers][D] of the pool's dtype; NULL = no norm), then the rotation to
+ * the token's logical position, then q to q_out and k, v to the cache. Sums
+ * and rotation in fp32, one rounding at the end; v is copied.
+ *   q: num_heads heads a token (NULL: keys and values only); q_out
+ *   [num_layers][num_tokens][num_heads][D] dense, may be q's own memory when q
+ *   is dense too. k, v: H_kv heads a token (both NULL: queries only).
+ *   positions [num_tokens] int32 logical positions (needed when rotating).
+ *   cache_pos [num_tokens] int32: the row of the token's sequence that k and v
+ *   go to, negative = nowhere (a padding token; its q is written all the same).
+ *   seqs [num_tokens] int32: the token's sequence, NULL = token n belongs to
+ *   sequence n. table NULL: cache_pos is the row of the pool itself (seqs and
+ *   num_seqs are not used), for a packed cache.
+ * Two tokens must not name the same row. Rules: INVALID_ARG for negative
+ * counts, eps < 0 or not finite, misaligned rows, seqs NULL with num_tokens >
+ * num_seqs, k without v; UNSUPPORTED for a rot_dim that is no multiple of 16 or
+ * above D, and for num_heads + 2 * H_kv > 65535. Device status: BAD_INDEX
+ * for a sequence, row or page out of range (that token's k and v are not
+ * written). Asynchronous; capturable. */
+kvsel_status kvsel_paged_append(const kvsel_pages* pages, int32_t num_tokens, int32_t num_heads,
+                                const kvsel_rows* q, const kvsel_rows* k, const kvsel_rows* v,
+                                const kvsel_rope* rope, const void* q_weight,
+                                const void* k_weight, float eps, const int32_t* positions,
+                                int32_t num_seqs, const int32_t* table, int32_t table_width,
+                                const int32_t* seqs, const int32_t* cache_pos, void* q_out,
+                                void* stream);
+
+/* kvsel_decode_attention over a paged cache: one query per (layer, sequence,
+ * query head) attends to the first lens[b] rows of its sequence. q
+ * [num_layers][num_seqs][num_heads][D] (the pool's dtype, 16-byte aligned),
+ * query head h reads cache head h / (num_heads / H_kv). out
+ * [num_layers][num_seqs][num_heads][D] fp32 (16-byte aligned), lse
+ * [num_layers][num_seqs][num_heads] fp32 natural log, or NULL. A sequence of
+ * length 0 gets out = 0, lse = -inf. Rows behind the length are never read.
+ * workspace: kvsel_paged_attention_bytes(pages, num_seqs, num_heads) bytes, 16-byte
+ * aligned. Repeated calls on the same inputs give the same bits. Rules:
+ * INVALID_ARG for num_heads that H_kv does not divide, a workspace that is too
+ * small or misaligned; UNSUPPORTED for num_seqs > 8192 or num_layers * num_seqs *
+ * num_heads >= 2^31. Device status: BAD_INDEX for a length outside
+ * [0, table_width * page_size] (taken as the nearer end) or a page out of range
+ * (its rows are left out), NONFINITE if a sum or an output is not finite.
+ * Asynchronous; capturable. */
+kvsel_status kvsel_paged_attention(const kvsel_pages* pages, int32_t num_seqs, int32_t num_heads,
+                                   const void* q, const int32_t* table, int32_t table_width,
+                                   const int32_t* lens, float* out, float* lse, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of kvsel_paged_attention on the current device, or -1 if a rule is
+ * broken. Does not depend on the lengths. Host only. */
+int64_t kvsel_paged_attention_bytes(const kvsel_pages* pages, int32_t num_seqs,
+                                    int32_t num_heads);
+
+/* Cuts paged caches to their kept rows, in place. keep_idx
+ * [num_layers][keep_rows][H_kv] int32 (kvsel_select's or kvsel_snapkv_grouped's
+ * out_idx, any order): entries keep_offsets[b] .. keep_offsets[b+1]-1 are sequence
+ * b's kept rows, n of them, distinct, in [0, lens[b]). Afterwards slots 0 .. n-1
+ * of the sequence hold the kept rows: a kept row j < n stays at slot j, and the
+ * slots left over, ascending, take the kept rows j >= n in the list's order (a
+ * future query's result does not depend on the order of the rows). Only rows
+ * that change their slot are read and written; what lies in slots >= n is
+ * left as it is, and kvsel_pages_update then frees their pages. slot_pos
+ * [num_layers][keep_rows][H_kv] int32 (or NULL): the row that each slot now holds.
+ * keep_offsets [num_seqs + 1] int32 on the device, nondecreasing from 0.
+ * max_keep: an upper bound on n. ref [num_pages] int32 (or NULL: not checked): the
+ * references from kvsel_pages_update; a sequence whose slots 0 .. n-1 touch a page with
+ * ref > 1 while n < lens[b] is left whole and SHARED_PAGE recorded.
+ * Rules: INVALID_ARG for num_seqs < 0, max_keep < 0, keep_rows < 0; UNSUPPORTED for
+ * max_keep > 32768 or num_layers * num_seqs * H_kv >= 2^31. Device status: BAD_INDEX for
+ * offsets, lengths or pages out of range, n > max_keep, n > lens[b], a kept row outside
+ * [0, lens[b]) or named twice below n (that layer's and head's rows of the
+ * sequence are left as they were, its slot_pos too).
+ * Asynchronous; capturable. */
+kvsel_status kvsel_paged_compact(const kvsel_pages* pages, int32_t num_seqs, const int32_t* table,
+                                 int32_t table_width, const int32_t* lens,
+                                 const int32_t* keep_idx, int64_t keep_rows,
+                                 const int32_t* keep_offsets, int32_t max_keep,
+                                 const int32_t* ref, int32_t* slot_pos, void* stream);
+
+/* One step of a pool's bookkeeping: from the num_in sequences (table, lens) to
+ * num_out sequences (table_out, new_lens). New sequence b goes on from old
+ * sequence parents[b] (-1: from nothing; parents NULL: from sequence b, num_in ==
+ * num_out) with its first m = min(lens[parent], new_lens[b]) rows, and gets
+ * pages for new_lens[b] rows: rows m and later are the caller's to write. So one
+ * call forks, reorders beams, grows for the next token, cuts and frees (a page
+ * that no new sequence holds is free). Pages that are whole within the m rows
+ * are shared; the page of a started row group (m % page_size > 0) stays with the
+ * lowest b that continues it, if no sequence holds it whole, and the others get a
+ * copy of its m % page_size rows (every layer, K and V). Pages are handed out
+ * lowest number first, in the order of (b, column). The result depends only on
+ * the arguments; table_out must not overlap table.
+ *   table_out [num_out][table_width] int32, -1 past the pages held; ref
+ *   [num_pages] int32: how many new sequences hold each page; free_pages [1] int32
+ *   (or NULL): pages left free, negative = pages that were missing (their entries
+ *   are -1, NO_PAGES is recorded).
+ * workspace: kvsel_pages_update_bytes(pages, num_out) bytes, 16-byte aligned. Rules:
+ * INVALID_ARG for negative counts, a workspace that is too small or misaligned,
+ * parents NULL with num_in != num_out; UNSUPPORTED for num_out * table_width >=
+ * 2^31. Device status: BAD_INDEX for a parent, length or page out of range (such a
+ * sequence becomes empty; such a page's entry becomes -1).
+ * Asynchronous; capturable. */
+kvsel_status kvsel_pages_update(const kvsel_pages* pages, int32_t num_in, const int32_t* table,
+                                int32_t table_width, const int32_t* lens, int32_t num_out,
+                                const int32_t* parents, const int32_t* new_lens,
+                                int32_t* table_out, int32_t* ref, int32_t* free_pages,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of kvsel_pages_update, or -1 if a rule is broken. Host only. */
+int64_t kvsel_pages_update_bytes(const kvsel_pages* pages, int32_t num_out);
 
 /* Synchronises `stream`, then returns and clears the current device's status
  * word: the first device-side error recorded since the last call, or

@@ -20,7 +20,28 @@ class KvselShape(ctypes.Structure):
                 ("seq_offsets", ctypes.POINTER(c_i64))]
 
 
+class KvselPages(ctypes.Structure):
+    """Mirror of ``kvsel_pages``."""
+    _fields_ = [("num_layers", c_i32), ("num_pages", c_i32), ("page_size", c_i32),
+                ("num_kv_heads", c_i32), ("head_dim", c_i32), ("dtype", c_i32),
+                ("layer_stride", c_i64), ("page_stride", c_i64), ("K", c_vp), ("V", c_vp)]
+
+
+class KvselRows(ctypes.Structure):
+    """Mirror of ``kvsel_rows``."""
+    _fields_ = [("data", c_vp), ("layer_stride", c_i64), ("token_stride", c_i64)]
+
+
+class KvselRope(ctypes.Structure):
+    """Mirror of ``kvsel_rope``."""
+    _fields_ = [("rot_dim", c_i32), ("interleaved", c_i32), ("inv_freq", c_vp),
+                ("scale", ctypes.c_float)]
+
+
 _P = ctypes.POINTER(KvselShape)
+_PG = ctypes.POINTER(KvselPages)
+_R = ctypes.POINTER(KvselRows)
+c_f32, c_f64 = ctypes.c_float, ctypes.c_double
 
 SIGNATURES = {
     "kvsel_version": (ctypes.c_char_p, []),
@@ -50,6 +71,19 @@ SIGNATURES = {
     "kvsel_reverse_attention": (c_i32, [_P, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "kvsel_cache_lengths": (c_i32, [_P, c_i32, c_i32, ctypes.POINTER(c_i64),
                                     ctypes.POINTER(c_i64)]),
+    "kvsel_rope_frequencies": (c_i32, [c_i32, c_f64, c_i32, c_f64, c_i64, c_f64, c_f64,
+                                       ctypes.POINTER(c_f32), ctypes.POINTER(c_f32)]),
+    "kvsel_paged_append": (c_i32, [_PG, c_i32, c_i32, _R, _R, _R, ctypes.POINTER(KvselRope),
+                                   c_vp, c_vp, c_f32, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp,
+                                   c_vp]),
+    "kvsel_paged_attention": (c_i32, [_PG, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp,
+                                      c_vp, c_i64, c_vp]),
+    "kvsel_paged_attention_bytes": (c_i64, [_PG, c_i32, c_i32]),
+    "kvsel_paged_compact": (c_i32, [_PG, c_i32, c_vp, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp,
+                                    c_vp, c_vp]),
+    "kvsel_pages_update": (c_i32, [_PG, c_i32, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
+                                   c_vp, c_vp, c_i64, c_vp]),
+    "kvsel_pages_update_bytes": (c_i64, [_PG, c_i32]),
     "kvsel_device_status": (c_i32, [c_vp]),
     "kvsel_set_wait_limit_ns": (c_i32, [c_u64]),
     "kvsel_debug_inject": (c_i32, [c_i32]),

@@ -12,6 +12,13 @@ states:
 host sequence of S + 1 token offsets. Work is queued on the current torch
 stream (or ``stream``); call ``kvsel_device_status`` to learn about errors
 only the GPU can see.
+
+The paged-cache calls (``kvsel_paged_*``, ``kvsel_pages_update``) take a pool
+K, V [layers, pages, page_size, H_kv, D] (one layer: 4-D), a table
+[S, table_width] int32 of page numbers and lengths [S] int32, all on one
+device, which need not be the current one. The last three dimensions of the
+pool are dense, layers and pages may be strided. Outputs and workspaces that
+the caller does not pass are allocated on the stream the call runs on.
 """
 
 from __future__ import annotations
@@ -30,10 +37,16 @@ KVSEL_ERR_NONFINITE = 3
 KVSEL_ERR_TIMEOUT = 4
 KVSEL_ERR_CUDA = 5
 KVSEL_ERR_BAD_INDEX = 6
+KVSEL_ERR_NO_PAGES = 7
+KVSEL_ERR_SHARED_PAGE = 8
 KVSEL_POOL_AVG = 0
 KVSEL_POOL_MAX = 1
 KVSEL_BF16 = 0
 KVSEL_F32 = 1
+KVSEL_ROPE_PLAIN = 0
+KVSEL_ROPE_LINEAR = 1
+KVSEL_ROPE_BASE = 2
+KVSEL_ROPE_PARTS = 3
 
 _DTYPES = {torch.bfloat16: KVSEL_BF16, torch.float32: KVSEL_F32}
 
@@ -431,6 +444,262 @@ def kvsel_cache_lengths(seq_offsets, C: int, g: int):
     _check(_native.lib().kvsel_cache_lengths(sh.ref, int(C), int(g), phys, logi),
            "kvsel_cache_lengths")
     return [phys[i] for i in range(n)], [logi[i] for i in range(n)]
+
+
+# ---------------------------------------------------------------------------
+# Paged caches
+# ---------------------------------------------------------------------------
+
+class _On:
+    """Device and stream of a paged call: makes the tensors' device current, and
+    the given stream torch's current one (so that allocations belong to it)."""
+
+    def __init__(self, device, stream):
+        self.handle = None
+        self._guards = []
+        if device.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.device != device:
+                raise ValueError("the stream must be on the tensors' device")
+            self._guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def _dev(device, **tensors) -> None:
+    """Every tensor given is a contiguous int32 tensor on `device`."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _pool(K: torch.Tensor, V: torch.Tensor) -> _native.KvselPages:
+    if K.dim() == 4:
+        K, V = K.unsqueeze(0), V.unsqueeze(0)
+    if K.dim() != 5 or K.shape != V.shape or K.dtype != V.dtype or K.device != V.device:
+        raise ValueError("K and V must be [layers, pages, page_size, H_kv, D] of one shape, type "
+                         "and device")
+    if not K.is_cuda:
+        raise ValueError("K must be a CUDA tensor")
+    if K.dtype not in _DTYPES:
+        raise ValueError("K must be bf16 or fp32")
+    layers, pages, ps, hkv, d = K.shape
+    ls, pg, *inner = K.stride()
+    dense = [hkv * d, d, 1]
+    for t in (K, V):
+        if any(n > 1 and s != w for n, s, w in zip((ps, hkv, d), t.stride()[2:], dense)):
+            raise ValueError("K and V must be dense in their last three dimensions")
+    if V.stride()[:2] != (ls, pg) and K.numel():
+        raise ValueError("K and V must have the same strides")
+    # a stride of a dimension of one entry means nothing
+    page = ps * hkv * d
+    return _native.KvselPages(layers, pages, ps, hkv, d, _DTYPES[K.dtype],
+                              0 if layers == 1 else ls, pg if pages > 1 else page,
+                              K.data_ptr(), V.data_ptr())
+
+
+def _workspace(workspace, need: int, device):
+    if need < 0:
+        raise KvselError(KVSEL_ERR_INVALID_ARG, "workspace")
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    return workspace
+
+
+def _rows_of(t: torch.Tensor, name: str, K: torch.Tensor, tokens: int, heads: int):
+    """kvsel_rows of a [layers, tokens, heads, D] tensor (one layer: 3-D)."""
+    t = _as4(t)
+    layers = 1 if K.dim() == 4 else K.shape[0]
+    if tuple(t.shape) != (layers, tokens, heads, K.shape[-1]):
+        raise ValueError(f"{name} must be {(layers, tokens, heads, K.shape[-1])}, got {tuple(t.shape)}")
+    if t.dtype != K.dtype or t.device != K.device:
+        raise ValueError(f"{name} must have the cache's type and device")
+    ls, ts, hs, es = t.stride()
+    if (heads > 1 and hs != t.shape[3]) or es != 1:
+        raise ValueError(f"{name} must be dense in its last two dimensions")
+    return _native.KvselRows(t.data_ptr(), ls if layers > 1 else 0, ts if tokens > 1 else 0)
+
+
+def kvsel_rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = KVSEL_ROPE_PLAIN,
+                           factor: float = 1.0, original_len: int = 1, low: float = 1.0,
+                           high: float = 32.0) -> Tuple[torch.Tensor, float]:
+    """(inv_freq [rot_dim / 2] fp32 CPU tensor, scale) of a rotation; `kind` one of KVSEL_ROPE_*."""
+    out = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.float32)
+    scale = ctypes.c_float(1.0)
+    _check(_native.lib().kvsel_rope_frequencies(
+        int(rot_dim), float(base), int(kind), float(factor), int(original_len), float(low),
+        float(high), ctypes.cast(out.data_ptr(), ctypes.POINTER(ctypes.c_float)),
+        ctypes.byref(scale)), "kvsel_rope_frequencies")
+    return out, scale.value
+
+
+def kvsel_paged_append(q, k, v, K, V, cache_pos, positions=None, table=None, seqs=None,
+                       q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None,
+                       interleaved: bool = False, scale: float = 1.0, q_out=None, stream=None):
+    """Norm, rotation and cache rows of new tokens; returns q_out [layers, N, H, D] (None
+    without q). q [layers, N, H, D], k, v [layers, N, H_kv, D]: dense in the last two
+    dimensions (one layer: 3-D). inv_freq [rot_dim / 2] fp32 (None: no rotation)."""
+    pool = _pool(K, V)
+    dev = K.device
+    if q is None and k is None:
+        raise ValueError("q or k and v must be given")
+    if (k is None) != (v is None):
+        raise ValueError("k and v go together")
+    first = _as4(q if q is not None else k)
+    n = first.shape[1]
+    layers = pool.num_layers
+    _dev(dev, cache_pos=cache_pos, positions=positions, table=table, seqs=seqs)
+    if k is not None and (cache_pos is None or cache_pos.numel() != n):
+        raise ValueError("cache_pos must have one entry a token")
+    if seqs is not None and seqs.numel() != n:
+        raise ValueError("seqs must have one entry a token")
+    if table is not None and table.dim() != 2:
+        raise ValueError("table must be [num_seqs, table_width]")
+    rope = None
+    if inv_freq is not None and inv_freq.numel():
+        if inv_freq.dtype != torch.float32 or inv_freq.device != dev or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous fp32 tensor on the cache's device")
+        if positions is None or positions.numel() != n:
+            raise ValueError("positions must have one entry a token")
+        rope = _native.KvselRope(2 * inv_freq.numel(), int(bool(interleaved)), inv_freq.data_ptr(),
+                                 float(scale))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != K.dtype or w.device != dev or not w.is_contiguous() or
+                              w.numel() != layers * pool.head_dim):
+            raise ValueError(f"{name} must be a contiguous [layers, D] tensor of the cache's type")
+    rq = rk = rv = None
+    heads = 0
+    if q is not None:
+        heads = first.shape[2]
+        rq = _rows_of(q, "q", K, n, heads)
+    if k is not None:
+        rk, rv = (_rows_of(x, m, K, n, pool.num_kv_heads) for x, m in ((k, "k"), (v, "v")))
+    with _On(dev, stream) as on:
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=K.dtype, device=dev)
+            if q_out.shape != q.shape or q_out.device != dev:
+                raise ValueError("q_out must have q's shape and device")
+            _need(q_out, "q_out", K.dtype)
+        ref = ctypes.byref
+        _check(_native.lib().kvsel_paged_append(
+            ref(pool), n, heads, ref(rq) if rq else None, ref(rk) if rk else None,
+            ref(rv) if rv else None, ref(rope) if rope else None, _ptr(q_weight), _ptr(k_weight),
+            float(eps), _ptr(positions), 0 if table is None else table.shape[0], _ptr(table),
+            0 if table is None else table.shape[1], _ptr(seqs), _ptr(cache_pos),
+            _ptr(q_out) if q is not None else None, on.handle), "kvsel_paged_append")
+    return q_out if q is not None else None
+
+
+def kvsel_paged_attention(q, K, V, table, lens, out=None, lse=None, want_lse: bool = True,
+                          workspace=None, stream=None):
+    """(out [layers, S, H, D] fp32, lse [layers, S, H] fp32 or None): one query per (layer,
+    sequence, query head) over the first lens[b] rows of its pages. q [layers, S, H, D] (one
+    layer: 3-D, like the pool 4-D)."""
+    pool = _pool(K, V)
+    dev = K.device
+    q4 = _as4(q)
+    L, S, H, D = q4.shape
+    if L != pool.num_layers or D != pool.head_dim or q.dtype != K.dtype or q.device != dev:
+        raise ValueError("q must be [layers, S, H, D] of the cache's layers, D, type and device")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _dev(dev, table=table, lens=lens)
+    if table.dim() != 2 or table.shape[0] != S or lens.numel() != S:
+        raise ValueError("table must be [S, table_width] and lens [S]")
+    with _On(dev, stream) as on:
+        lib = _native.lib()
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        for name, t, n in (("out", out, q.numel()), ("lse", lse, L * S * H)):
+            if t is not None and (t.dtype != torch.float32 or t.device != dev or t.numel() != n or
+                                  not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous fp32 tensor of {n} entries")
+        ref = ctypes.byref(pool)
+        ws = _workspace(workspace, lib.kvsel_paged_attention_bytes(ref, S, H), dev)
+        _check(lib.kvsel_paged_attention(ref, S, H, _ptr(q), _ptr(table), table.shape[1], _ptr(lens),
+                                         _ptr(out), _ptr(lse), _ptr(ws),
+                                         ws.numel() * ws.element_size(), on.handle),
+               "kvsel_paged_attention")
+    return out, lse
+
+
+def kvsel_paged_compact(K, V, table, lens, keep_idx, keep_offsets, max_keep: int, ref=None,
+                        slot_pos=None, stream=None):
+    """slot_pos [layers, keep_rows, H_kv] int32: the cache cut in place to the rows that
+    keep_idx [layers, keep_rows, H_kv] names (sequence b's at keep_offsets[b] ..)."""
+    pool = _pool(K, V)
+    dev = K.device
+    _dev(dev, table=table, lens=lens, keep_idx=keep_idx, keep_offsets=keep_offsets, ref=ref,
+         slot_pos=slot_pos)
+    k3 = keep_idx if keep_idx.dim() == 3 else keep_idx.unsqueeze(0)
+    S = table.shape[0]
+    if k3.shape[0] != pool.num_layers or k3.shape[2] != pool.num_kv_heads:
+        raise ValueError("keep_idx must be [layers, keep_rows, H_kv]")
+    if lens.numel() != S or keep_offsets.numel() != S + 1:
+        raise ValueError("lens must have S entries and keep_offsets S + 1")
+    if ref is not None and ref.numel() != pool.num_pages:
+        raise ValueError("ref must have one entry a page")
+    with _On(dev, stream) as on:
+        if slot_pos is None:
+            slot_pos = torch.empty_like(keep_idx)
+        if slot_pos.shape != keep_idx.shape:
+            raise ValueError("slot_pos must have keep_idx's shape")
+        _check(_native.lib().kvsel_paged_compact(
+            ctypes.byref(pool), S, _ptr(table), table.shape[1], _ptr(lens), _ptr(keep_idx),
+            k3.shape[1], _ptr(keep_offsets), int(max_keep), _ptr(ref), _ptr(slot_pos), on.handle),
+            "kvsel_paged_compact")
+    return slot_pos
+
+
+def kvsel_pages_update(K, V, table, lens, new_lens, parents=None, table_out=None, ref=None,
+                       free_pages=None, workspace=None, stream=None):
+    """(table_out [num_out, table_width], ref [pages], free_pages [1]), int32: the tables of the
+    next step's sequences; new sequence b goes on from old sequence parents[b] (-1: none; None:
+    b) and holds pages for new_lens[b] rows."""
+    pool = _pool(K, V)
+    dev = K.device
+    _dev(dev, table=table, lens=lens, new_lens=new_lens, parents=parents, table_out=table_out,
+         ref=ref, free_pages=free_pages)
+    n_in, width = table.shape
+    n_out = new_lens.numel()
+    if lens.numel() != n_in or (parents is not None and parents.numel() != n_out):
+        raise ValueError("lens must have one entry an old sequence, parents one a new one")
+    with _On(dev, stream) as on:
+        lib = _native.lib()
+        empty = lambda *n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
+        table_out = empty(n_out, width) if table_out is None else table_out
+        ref = empty(pool.num_pages) if ref is None else ref
+        free_pages = empty(1) if free_pages is None else free_pages
+        if (tuple(table_out.shape) != (n_out, width) or ref.numel() != pool.num_pages or
+                free_pages.numel() != 1):
+            raise ValueError("table_out must be [num_out, table_width], ref [pages], free_pages [1]")
+        p = ctypes.byref(pool)
+        ws = _workspace(workspace, lib.kvsel_pages_update_bytes(p, n_out), dev)
+        _check(lib.kvsel_pages_update(p, n_in, _ptr(table), width, _ptr(lens), n_out, _ptr(parents),
+                                      _ptr(new_lens), _ptr(table_out), _ptr(ref), _ptr(free_pages),
+                                      _ptr(ws), ws.numel() * ws.element_size(), on.handle),
+               "kvsel_pages_update")
+    return table_out, ref, free_pages
 
 
 def kvsel_device_status(stream=None) -> int:

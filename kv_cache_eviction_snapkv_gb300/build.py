@@ -27,7 +27,8 @@ LIB = os.path.join(PKG, "libkvsel.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libkvsel_debug.so")
 SOURCES = ["api.cu", "score_tc.cu", "score_generic.cu", "select.cu", "compact.cu",
-           "decode.cu", "jacap.cu", "reverse.cu"]
+           "decode.cu", "jacap.cu", "reverse.cu", "paged_api.cu", "paged_append.cu",
+           "paged_attention.cu", "paged_compact.cu", "pages_update.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -84,8 +84,7 @@ kvsel_status device_state(DevState** out) {
     void* p = nullptr;
     if ((e = cudaGetSymbolAddress(&p, g_status_word)))
       return cuda_fail(e, "cudaGetSymbolAddress(status word)");
-    d.status = static_cast<int*>(p);
-    if ((e = cudaMemset(d.status, 0, sizeof(int)))) return cuda_fail(e, "cudaMemset(status)");
+    d.status = static_cast<int*>(p);  // zero from the module's load on
     d.ready = true;
   }
   *out = &d;
@@ -467,6 +466,18 @@ size_t score_ws_bytes(const Plan& p, const ScorePlan& sp) {
 }
 
 }  // namespace
+
+kvsel_status device_info(DeviceInfo* out) {
+  DevState* d;
+  const kvsel_status st = device_state(&d);
+  if (st) return st;
+  out->sm_count = d->sm_count;
+  out->status = d->status;
+  return KVSEL_OK;
+}
+
+kvsel_status launch_status(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
 }  // namespace kvsel
 
 // ---------------------------------------------------------------------------
@@ -599,6 +610,8 @@ const char* kvsel_status_string(kvsel_status s) {
     case KVSEL_ERR_TIMEOUT: return "a bounded device wait ran out";
     case KVSEL_ERR_CUDA: return "CUDA runtime error";
     case KVSEL_ERR_BAD_INDEX: return "gather index out of range";
+    case KVSEL_ERR_NO_PAGES: return "too few free pages";
+    case KVSEL_ERR_SHARED_PAGE: return "a page to be rewritten is shared";
     default: return "unknown status";
   }
 }

@@ -288,4 +288,108 @@ cudaError_t launch_tc_score(const ScoreArgs& a, bool logits_mode, int grid);
 int tc_max_grid(int sm_count);                  // co-resident CTAs (one per SM)
 int tc_max_chunks(int W, int sm_count);         // most chunks one instance may have
 
+// ---------------------------------------------------------------------------
+// Paged caches
+// ---------------------------------------------------------------------------
+
+// What the entry points need to know of the current device.
+struct DeviceInfo {
+  int sm_count;
+  int* status;
+};
+kvsel_status device_info(DeviceInfo* out);
+kvsel_status launch_status(cudaError_t e, const char* what);
+
+// A pool as the kernels see it; a row is the H_kv heads of one cache slot.
+struct PagedView {
+  char* k;
+  char* v;
+  int64_t layer_bytes;
+  uint32_t page_units, row_units;  // in 32-byte units
+  uint32_t head_units;             // one head of a row
+  int page_size, page_shift;
+  int num_pages, layers, Hkv, D, dtype;
+};
+
+struct AppendArgs {
+  PagedView pv;
+  const char* src[3];       // q, k, v (null: absent)
+  int64_t layer_bytes[3];   // their strides
+  int64_t token_bytes[3];
+  char* q_out;
+  int tokens, H;
+  int rot, interleaved;
+  const float* inv_freq;
+  float rope_scale;
+  const char* weight[2];    // q, k norm weights [layers][D], or null
+  float eps;
+  const int32_t* positions;
+  const int32_t* table;     // null: cache_pos is the pool row
+  int table_width, num_seqs;
+  const int32_t* seqs;      // null: token n belongs to sequence n
+  const int32_t* cache_pos;
+  int* status;
+  int sm_count;
+  cudaStream_t stream;
+};
+
+struct PagedAttnArgs {
+  PagedView pv;
+  const void* q;            // [layers][S][H][D]
+  const int32_t* table;
+  int table_width;
+  const int32_t* lens;
+  int S, H;
+  float* out;               // [layers][S][H][D]
+  float* lse;               // [layers][S][H], or null
+  float scale_log2;         // log2(e) / sqrt(D)
+  char* ws;
+  int* status;
+  int sm_count;
+  cudaStream_t stream;
+};
+
+struct PagedCompactArgs {
+  PagedView pv;
+  const int32_t* table;
+  int table_width, S;
+  const int32_t* lens;
+  const int32_t* keep_idx;  // [layers][keep_rows][Hkv]
+  int64_t keep_rows;
+  const int32_t* keep_offsets;
+  int max_keep;
+  const int32_t* ref;       // or null
+  int32_t* slot_pos;        // or null
+  int* status;
+  int sm_count;
+  cudaStream_t stream;
+};
+
+struct PagesUpdateArgs {
+  PagedView pv;
+  int num_in, num_out, table_width;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* parents;   // or null
+  const int32_t* new_lens;
+  int32_t* table_out;
+  int32_t* ref;
+  int32_t* free_pages;      // or null
+  char* ws;
+  int* status;
+  int sm_count;
+  cudaStream_t stream;
+};
+
+constexpr int kRowUnit = 32;          // bytes of an addressing unit of PagedView
+constexpr int kMaxPagedSeqs = 8192;
+constexpr int kMaxKeep = 32768;      // largest max_keep: its slot lists fill shared memory
+
+cudaError_t launch_append(const AppendArgs& a);
+int64_t paged_attention_ws(const PagedView& pv, int S, int H, int sm_count);
+cudaError_t launch_paged_attention(const PagedAttnArgs& a);
+cudaError_t launch_paged_compact(const PagedCompactArgs& a);
+int64_t pages_update_ws(int num_pages, int num_out);
+cudaError_t launch_pages_update(const PagesUpdateArgs& a);
+
 }  // namespace kvsel

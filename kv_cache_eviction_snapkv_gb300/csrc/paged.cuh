@@ -1,0 +1,31 @@
+// Descriptors and device helpers shared by the paged-cache kernels.
+#pragma once
+
+#include "kvsel_device.cuh"
+
+namespace kvsel {
+
+// Offset of row r of a page within its layer, in units of 32 bytes: they fit 32
+// bits for pools of up to 128 GiB a layer (the host checks that).
+__device__ __forceinline__ uint32_t row_units(const PagedView& pv, int page, int r) {
+  return (uint32_t)page * pv.page_units + (uint32_t)r * pv.row_units;
+}
+
+// Page of column `col` of a sequence, or -1 (and BAD_INDEX) if it is not one
+// of the pool's.
+__device__ __forceinline__ int checked_page(const PagedView& pv, const int32_t* table_row, int col,
+                                            int* status) {
+  const int page = __ldg(table_row + col);
+  if (page >= 0 && page < pv.num_pages) return page;
+  record_status(status, KVSEL_ERR_BAD_INDEX);
+  return -1;
+}
+
+// Length of a sequence, held to [0, max_rows].
+__device__ __forceinline__ int checked_len(int len, int max_rows, int* status) {
+  if (len >= 0 && len <= max_rows) return len;
+  record_status(status, KVSEL_ERR_BAD_INDEX);
+  return len < 0 ? 0 : max_rows;
+}
+
+}  // namespace kvsel
