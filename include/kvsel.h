@@ -447,7 +447,7 @@ kvsel_status kvsel_paged_append(const kvsel_pages* pages, int32_t num_tokens, in
 
 /* kvsel_decode_attention over a paged cache: one query per (layer, sequence,
  * query head) attends to the first lens[b] rows of its sequence. q
- * [num_layers][num_seqs][num_heads][D] (the pool's dtype, 16-byte aligned),
+ * [num_layers][num_seqs][num_heads][D] (the pool's dtype, 32-byte aligned),
  * query head h reads cache head h / (num_heads / H_kv). out
  * [num_layers][num_seqs][num_heads][D] fp32 (16-byte aligned), lse
  * [num_layers][num_seqs][num_heads] fp32 natural log, or NULL. A sequence of
@@ -455,8 +455,8 @@ kvsel_status kvsel_paged_append(const kvsel_pages* pages, int32_t num_tokens, in
  * workspace: kvsel_paged_attention_bytes(pages, num_seqs, num_heads) bytes, 16-byte
  * aligned. Repeated calls on the same inputs give the same bits. Rules:
  * INVALID_ARG for num_heads that H_kv does not divide, a workspace that is too
- * small or misaligned; UNSUPPORTED for num_seqs > 8192 or num_layers * num_seqs *
- * num_heads >= 2^31. Device status: BAD_INDEX for a length outside
+ * small or misaligned; UNSUPPORTED for num_seqs > 8192, num_layers * num_seqs *
+ * num_heads >= 2^31 or num_seqs * table_width * page_size > 2^35. Device status: BAD_INDEX for a length outside
  * [0, table_width * page_size] (taken as the nearer end) or a page out of range
  * (its rows are left out), NONFINITE if a sum or an output is not finite.
  * Asynchronous; capturable. */

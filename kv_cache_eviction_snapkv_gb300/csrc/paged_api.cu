@@ -190,7 +190,9 @@ kvsel_status kvsel_paged_attention(const kvsel_pages* pages, int32_t num_seqs, i
   if ((st = attention_view(pages, true, num_seqs, num_heads, &a.pv))) return st;
   if ((st = check_table(a.pv, num_seqs, table, table_width))) return st;
   if (num_seqs == 0) return KVSEL_OK;
-  if (!q || !lens || !out || misaligned(q, 16) || misaligned(out, 16))
+  if ((int64_t)num_seqs * table_width > (int64_t(1) << 35) / a.pv.page_size)
+    return KVSEL_ERR_UNSUPPORTED;
+  if (!q || !lens || !out || misaligned(q, kRowUnit) || misaligned(out, 16))
     return KVSEL_ERR_INVALID_ARG;
   DeviceInfo d;
   if ((st = device_info(&d))) return st;

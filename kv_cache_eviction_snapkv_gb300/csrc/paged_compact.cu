@@ -136,11 +136,12 @@ __global__ void __launch_bounds__(kThreads) paged_compact_kernel(const __grid_co
 }  // namespace
 
 cudaError_t launch_paged_compact(const PagedCompactArgs& a) {
-  const int smem = ((a.max_keep + 31) >> 5) * 4 + 2 * ((a.max_keep + 1) & ~1) * 2;
-  static_assert((kMaxKeep / 32) * 4 + 4 * kMaxKeep <= 227 * 1024, "slot lists fit shared memory");
+  auto lists = [](int n) { return ((n + 31) >> 5) * 4 + 2 * ((n + 1) & ~1) * 2; };
+  const int smem = lists(a.max_keep);
   if (smem > 48 * 1024) {
+    // always the same value: another thread's call may come between
     const cudaError_t e = cudaFuncSetAttribute(
-        paged_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        paged_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lists(kMaxKeep));
     if (e) return e;
   }
   const int64_t insts = (int64_t)a.pv.layers * a.S * a.pv.Hkv;
