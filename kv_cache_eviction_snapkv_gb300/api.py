@@ -23,6 +23,7 @@ the caller does not pass are allocated on the stream the call runs on.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence, Tuple
 
@@ -450,89 +451,89 @@ def kvsel_cache_lengths(seq_offsets, C: int, g: int):
 # Paged caches
 # ---------------------------------------------------------------------------
 
-class _On:
-    """Device and stream of a paged call: makes the tensors' device current, and
-    the given stream torch's current one (so that allocations belong to it)."""
-
-    def __init__(self, device, stream):
-        self.handle = None
-        self._guards = []
-        if device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(device))
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            if stream.device != device:
-                raise ValueError("the stream must be on the tensors' device")
-            self._guards.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        self.handle = torch.cuda.current_stream().cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
+_raw_stream = torch._C._cuda_getCurrentRawStream   # a stream's handle without the object around it
 
 
-def _dev(device, **tensors) -> None:
-    """Every tensor given is a contiguous int32 tensor on `device`."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+@contextlib.contextmanager
+def _on(device: int, stream):
+    """Makes the tensors' device current and the given stream torch's current one, so that what
+    a call allocates belongs to the stream that it runs on."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device.index != device:
+            raise ValueError("the stream must be on the tensors' device")
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _elsewhere(device: int, stream) -> bool:
+    """Whether a call on `device` needs `_on` (another device or stream than the current ones)."""
+    return stream is not None or device != torch.cuda.current_device()
+
+
+def _i32(t: torch.Tensor, name: str, device: int) -> int:
+    """Address of a contiguous int32 tensor on `device`."""
+    if t.dtype is not torch.int32 or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device")
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], name: str, device: int) -> Optional[int]:
+    return None if t is None else _i32(t, name, device)
 
 
 def _pool(K: torch.Tensor, V: torch.Tensor) -> _native.KvselPages:
-    if K.dim() == 4:
-        K, V = K.unsqueeze(0), V.unsqueeze(0)
-    if K.dim() != 5 or K.shape != V.shape or K.dtype != V.dtype or K.device != V.device:
-        raise ValueError("K and V must be [layers, pages, page_size, H_kv, D] of one shape, type "
-                         "and device")
+    shape, stride, code = K.shape, K.stride(), _DTYPES.get(K.dtype)
+    if V.shape != shape or V.dtype is not K.dtype or V.get_device() != K.get_device():
+        raise ValueError("K and V must have one shape, type and device")
     if not K.is_cuda:
         raise ValueError("K must be a CUDA tensor")
-    if K.dtype not in _DTYPES:
+    if code is None:
         raise ValueError("K must be bf16 or fp32")
-    layers, pages, ps, hkv, d = K.shape
-    ls, pg, *inner = K.stride()
-    dense = [hkv * d, d, 1]
-    for t in (K, V):
-        if any(n > 1 and s != w for n, s, w in zip((ps, hkv, d), t.stride()[2:], dense)):
-            raise ValueError("K and V must be dense in their last three dimensions")
-    if V.stride()[:2] != (ls, pg) and K.numel():
+    if len(shape) == 4:
+        layers, ls = 1, 0
+        pages, ps, hkv, d = shape
+        pg, s2, s3, s4 = stride
+    elif len(shape) == 5:
+        layers, pages, ps, hkv, d = shape
+        ls, pg, s2, s3, s4 = stride
+    else:
+        raise ValueError("K and V must be [layers, pages, page_size, H_kv, D]")
+    # the stride of a dimension of one entry means nothing
+    if (s4 != 1 and d > 1) or (s3 != d and hkv > 1) or (s2 != hkv * d and ps > 1):
+        raise ValueError("K and V must be dense in their last three dimensions")
+    if V.stride() != stride and any(n > 1 and x != y for n, x, y in zip(shape, stride, V.stride())):
         raise ValueError("K and V must have the same strides")
-    # a stride of a dimension of one entry means nothing
-    page = ps * hkv * d
-    return _native.KvselPages(layers, pages, ps, hkv, d, _DTYPES[K.dtype],
-                              0 if layers == 1 else ls, pg if pages > 1 else page,
-                              K.data_ptr(), V.data_ptr())
+    return _native.KvselPages(layers, pages, ps, hkv, d, code, ls if layers > 1 else 0,
+                              pg if pages > 1 else 0, K.data_ptr(), V.data_ptr())
 
 
-def _workspace(workspace, need: int, device):
-    if need < 0:
-        raise KvselError(KVSEL_ERR_INVALID_ARG, "workspace")
+def _workspace(workspace, need: int, K: torch.Tensor) -> torch.Tensor:
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
+        if need < 0:
+            raise KvselError(KVSEL_ERR_INVALID_ARG, "workspace")
+        return torch.empty(need, dtype=torch.uint8, device=K.device)
+    if workspace.get_device() != K.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     return workspace
 
 
-def _rows_of(t: torch.Tensor, name: str, K: torch.Tensor, tokens: int, heads: int):
+def _rows_of(t: torch.Tensor, name: str, K: torch.Tensor, layers: int, tokens: int, heads: int,
+             dim: int) -> _native.KvselRows:
     """kvsel_rows of a [layers, tokens, heads, D] tensor (one layer: 3-D)."""
-    t = _as4(t)
-    layers = 1 if K.dim() == 4 else K.shape[0]
-    if tuple(t.shape) != (layers, tokens, heads, K.shape[-1]):
-        raise ValueError(f"{name} must be {(layers, tokens, heads, K.shape[-1])}, got {tuple(t.shape)}")
-    if t.dtype != K.dtype or t.device != K.device:
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        shape, stride = (1, *shape), (0, *stride)
+    if shape != (layers, tokens, heads, dim):
+        raise ValueError(f"{name} must be {(layers, tokens, heads, dim)}, got {tuple(t.shape)}")
+    if t.dtype is not K.dtype or t.get_device() != K.get_device():
         raise ValueError(f"{name} must have the cache's type and device")
-    ls, ts, hs, es = t.stride()
-    if (heads > 1 and hs != t.shape[3]) or es != 1:
+    ls, ts, hs, es = stride
+    if (heads > 1 and hs != dim) or es != 1:
         raise ValueError(f"{name} must be dense in its last two dimensions")
     return _native.KvselRows(t.data_ptr(), ls if layers > 1 else 0, ts if tokens > 1 else 0)
 
@@ -557,54 +558,62 @@ def kvsel_paged_append(q, k, v, K, V, cache_pos, positions=None, table=None, seq
     without q). q [layers, N, H, D], k, v [layers, N, H_kv, D]: dense in the last two
     dimensions (one layer: 3-D). inv_freq [rot_dim / 2] fp32 (None: no rotation)."""
     pool = _pool(K, V)
-    dev = K.device
+    dev = K.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kvsel_paged_append(q, k, v, K, V, cache_pos, positions, table, seqs, q_weight,
+                                      k_weight, eps, inv_freq, interleaved, scale, q_out)
     if q is None and k is None:
         raise ValueError("q or k and v must be given")
     if (k is None) != (v is None):
         raise ValueError("k and v go together")
-    first = _as4(q if q is not None else k)
-    n = first.shape[1]
-    layers = pool.num_layers
-    _dev(dev, cache_pos=cache_pos, positions=positions, table=table, seqs=seqs)
-    if k is not None and (cache_pos is None or cache_pos.numel() != n):
-        raise ValueError("cache_pos must have one entry a token")
-    if seqs is not None and seqs.numel() != n:
-        raise ValueError("seqs must have one entry a token")
-    if table is not None and table.dim() != 2:
-        raise ValueError("table must be [num_seqs, table_width]")
-    rope = None
+    layers, hkv, dim = pool.num_layers, pool.num_kv_heads, pool.head_dim
+    byref = ctypes.byref
+    rq = rk = rv = rope = at = out = None
+    heads = 0
+    if q is not None:
+        n, heads = q.shape[-3], q.shape[-2]
+        rq = byref(_rows_of(q, "q", K, layers, n, heads, dim))
+    else:
+        n = k.shape[-3]
+    if k is not None:
+        rk = byref(_rows_of(k, "k", K, layers, n, hkv, dim))
+        rv = byref(_rows_of(v, "v", K, layers, n, hkv, dim))
+        if cache_pos is None or cache_pos.numel() != n:
+            raise ValueError("cache_pos must have one entry a token")
+        at = _i32(cache_pos, "cache_pos", dev)
     if inv_freq is not None and inv_freq.numel():
-        if inv_freq.dtype != torch.float32 or inv_freq.device != dev or not inv_freq.is_contiguous():
+        if (inv_freq.dtype is not torch.float32 or inv_freq.get_device() != dev or
+                not inv_freq.is_contiguous()):
             raise ValueError("inv_freq must be a contiguous fp32 tensor on the cache's device")
         if positions is None or positions.numel() != n:
             raise ValueError("positions must have one entry a token")
-        rope = _native.KvselRope(2 * inv_freq.numel(), int(bool(interleaved)), inv_freq.data_ptr(),
-                                 float(scale))
+        rope = byref(_native.KvselRope(2 * inv_freq.numel(), 1 if interleaved else 0,
+                                       inv_freq.data_ptr(), scale))
+    if seqs is not None and seqs.numel() != n:
+        raise ValueError("seqs must have one entry a token")
+    n_seqs = width = 0
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError("table must be [num_seqs, table_width]")
+        n_seqs, width = table.shape
+    weights = []
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != K.dtype or w.device != dev or not w.is_contiguous() or
-                              w.numel() != layers * pool.head_dim):
+        if w is not None and (w.dtype is not K.dtype or w.get_device() != dev or
+                              not w.is_contiguous() or w.numel() != layers * dim):
             raise ValueError(f"{name} must be a contiguous [layers, D] tensor of the cache's type")
-    rq = rk = rv = None
-    heads = 0
+        weights.append(None if w is None else w.data_ptr())
     if q is not None:
-        heads = first.shape[2]
-        rq = _rows_of(q, "q", K, n, heads)
-    if k is not None:
-        rk, rv = (_rows_of(x, m, K, n, pool.num_kv_heads) for x, m in ((k, "k"), (v, "v")))
-    with _On(dev, stream) as on:
-        if q is not None:
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=K.dtype, device=dev)
-            if q_out.shape != q.shape or q_out.device != dev:
-                raise ValueError("q_out must have q's shape and device")
-            _need(q_out, "q_out", K.dtype)
-        ref = ctypes.byref
-        _check(_native.lib().kvsel_paged_append(
-            ref(pool), n, heads, ref(rq) if rq else None, ref(rk) if rk else None,
-            ref(rv) if rv else None, ref(rope) if rope else None, _ptr(q_weight), _ptr(k_weight),
-            float(eps), _ptr(positions), 0 if table is None else table.shape[0], _ptr(table),
-            0 if table is None else table.shape[1], _ptr(seqs), _ptr(cache_pos),
-            _ptr(q_out) if q is not None else None, on.handle), "kvsel_paged_append")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=K.dtype, device=K.device)
+        elif (q_out.shape != q.shape or q_out.get_device() != dev or q_out.dtype is not K.dtype or
+              not q_out.is_contiguous()):
+            raise ValueError("q_out must be contiguous, with q's shape, type and device")
+        out = q_out.data_ptr()
+    _check(_native.lib().kvsel_paged_append(
+        byref(pool), n, heads, rq, rk, rv, rope, weights[0], weights[1], eps,
+        _opt(positions, "positions", dev), n_seqs, _opt(table, "table", dev), width,
+        _opt(seqs, "seqs", dev), at, out, _raw_stream(dev)), "kvsel_paged_append")
     return q_out if q is not None else None
 
 
@@ -614,32 +623,36 @@ def kvsel_paged_attention(q, K, V, table, lens, out=None, lse=None, want_lse: bo
     sequence, query head) over the first lens[b] rows of its pages. q [layers, S, H, D] (one
     layer: 3-D, like the pool 4-D)."""
     pool = _pool(K, V)
-    dev = K.device
-    q4 = _as4(q)
-    L, S, H, D = q4.shape
-    if L != pool.num_layers or D != pool.head_dim or q.dtype != K.dtype or q.device != dev:
-        raise ValueError("q must be [layers, S, H, D] of the cache's layers, D, type and device")
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    _dev(dev, table=table, lens=lens)
+    dev = K.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kvsel_paged_attention(q, K, V, table, lens, out, lse, want_lse, workspace)
+    shape = q.shape
+    L, S, H, D = shape if len(shape) == 4 else (1, *shape)
+    if (L != pool.num_layers or D != pool.head_dim or q.dtype is not K.dtype or
+            q.get_device() != dev or not q.is_contiguous()):
+        raise ValueError("q must be contiguous [layers, S, H, D] of the cache's layers, D, type and "
+                         "device")
     if table.dim() != 2 or table.shape[0] != S or lens.numel() != S:
         raise ValueError("table must be [S, table_width] and lens [S]")
-    with _On(dev, stream) as on:
-        lib = _native.lib()
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-        for name, t, n in (("out", out, q.numel()), ("lse", lse, L * S * H)):
-            if t is not None and (t.dtype != torch.float32 or t.device != dev or t.numel() != n or
-                                  not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous fp32 tensor of {n} entries")
-        ref = ctypes.byref(pool)
-        ws = _workspace(workspace, lib.kvsel_paged_attention_bytes(ref, S, H), dev)
-        _check(lib.kvsel_paged_attention(ref, S, H, _ptr(q), _ptr(table), table.shape[1], _ptr(lens),
-                                         _ptr(out), _ptr(lse), _ptr(ws),
-                                         ws.numel() * ws.element_size(), on.handle),
-               "kvsel_paged_attention")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=K.device)
+    elif (out.dtype is not torch.float32 or out.get_device() != dev or out.shape != shape or
+          not out.is_contiguous()):
+        raise ValueError("out must be a contiguous fp32 tensor of q's shape")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=K.device)
+    elif (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != shape[:-1] or
+          not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 tensor [layers, S, H]")
+    lib = _native.lib()
+    ref = ctypes.byref(pool)
+    ws = _workspace(workspace, lib.kvsel_paged_attention_bytes(ref, S, H), K)
+    _check(lib.kvsel_paged_attention(ref, S, H, q.data_ptr(), _i32(table, "table", dev),
+                                     table.shape[1], _i32(lens, "lens", dev), out.data_ptr(),
+                                     None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                     ws.nbytes, _raw_stream(dev)), "kvsel_paged_attention")
     return out, lse
 
 
@@ -648,26 +661,29 @@ def kvsel_paged_compact(K, V, table, lens, keep_idx, keep_offsets, max_keep: int
     """slot_pos [layers, keep_rows, H_kv] int32: the cache cut in place to the rows that
     keep_idx [layers, keep_rows, H_kv] names (sequence b's at keep_offsets[b] ..)."""
     pool = _pool(K, V)
-    dev = K.device
-    _dev(dev, table=table, lens=lens, keep_idx=keep_idx, keep_offsets=keep_offsets, ref=ref,
-         slot_pos=slot_pos)
-    k3 = keep_idx if keep_idx.dim() == 3 else keep_idx.unsqueeze(0)
-    S = table.shape[0]
-    if k3.shape[0] != pool.num_layers or k3.shape[2] != pool.num_kv_heads:
+    dev = K.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kvsel_paged_compact(K, V, table, lens, keep_idx, keep_offsets, max_keep, ref,
+                                       slot_pos)
+    shape = keep_idx.shape
+    L, rows, H = shape if len(shape) == 3 else (1, *shape)
+    if L != pool.num_layers or H != pool.num_kv_heads:
         raise ValueError("keep_idx must be [layers, keep_rows, H_kv]")
+    S, width = table.shape
     if lens.numel() != S or keep_offsets.numel() != S + 1:
         raise ValueError("lens must have S entries and keep_offsets S + 1")
     if ref is not None and ref.numel() != pool.num_pages:
         raise ValueError("ref must have one entry a page")
-    with _On(dev, stream) as on:
-        if slot_pos is None:
-            slot_pos = torch.empty_like(keep_idx)
-        if slot_pos.shape != keep_idx.shape:
-            raise ValueError("slot_pos must have keep_idx's shape")
-        _check(_native.lib().kvsel_paged_compact(
-            ctypes.byref(pool), S, _ptr(table), table.shape[1], _ptr(lens), _ptr(keep_idx),
-            k3.shape[1], _ptr(keep_offsets), int(max_keep), _ptr(ref), _ptr(slot_pos), on.handle),
-            "kvsel_paged_compact")
+    if slot_pos is None:
+        slot_pos = torch.empty(shape, dtype=torch.int32, device=K.device)
+    elif slot_pos.shape != shape:
+        raise ValueError("slot_pos must have keep_idx's shape")
+    _check(_native.lib().kvsel_paged_compact(
+        ctypes.byref(pool), S, _i32(table, "table", dev), width, _i32(lens, "lens", dev),
+        _i32(keep_idx, "keep_idx", dev), rows, _i32(keep_offsets, "keep_offsets", dev), max_keep,
+        _opt(ref, "ref", dev), _i32(slot_pos, "slot_pos", dev), _raw_stream(dev)),
+        "kvsel_paged_compact")
     return slot_pos
 
 
@@ -677,28 +693,33 @@ def kvsel_pages_update(K, V, table, lens, new_lens, parents=None, table_out=None
     next step's sequences; new sequence b goes on from old sequence parents[b] (-1: none; None:
     b) and holds pages for new_lens[b] rows."""
     pool = _pool(K, V)
-    dev = K.device
-    _dev(dev, table=table, lens=lens, new_lens=new_lens, parents=parents, table_out=table_out,
-         ref=ref, free_pages=free_pages)
+    dev = K.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kvsel_pages_update(K, V, table, lens, new_lens, parents, table_out, ref,
+                                      free_pages, workspace)
     n_in, width = table.shape
     n_out = new_lens.numel()
     if lens.numel() != n_in or (parents is not None and parents.numel() != n_out):
         raise ValueError("lens must have one entry an old sequence, parents one a new one")
-    with _On(dev, stream) as on:
-        lib = _native.lib()
-        empty = lambda *n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
-        table_out = empty(n_out, width) if table_out is None else table_out
-        ref = empty(pool.num_pages) if ref is None else ref
-        free_pages = empty(1) if free_pages is None else free_pages
-        if (tuple(table_out.shape) != (n_out, width) or ref.numel() != pool.num_pages or
-                free_pages.numel() != 1):
-            raise ValueError("table_out must be [num_out, table_width], ref [pages], free_pages [1]")
-        p = ctypes.byref(pool)
-        ws = _workspace(workspace, lib.kvsel_pages_update_bytes(p, n_out), dev)
-        _check(lib.kvsel_pages_update(p, n_in, _ptr(table), width, _ptr(lens), n_out, _ptr(parents),
-                                      _ptr(new_lens), _ptr(table_out), _ptr(ref), _ptr(free_pages),
-                                      _ptr(ws), ws.numel() * ws.element_size(), on.handle),
-               "kvsel_pages_update")
+    device = K.device
+    if table_out is None:
+        table_out = torch.empty((n_out, width), dtype=torch.int32, device=device)
+    if ref is None:
+        ref = torch.empty(pool.num_pages, dtype=torch.int32, device=device)
+    if free_pages is None:
+        free_pages = torch.empty(1, dtype=torch.int32, device=device)
+    if (table_out.shape != (n_out, width) or ref.numel() != pool.num_pages or
+            free_pages.numel() != 1):
+        raise ValueError("table_out must be [num_out, table_width], ref [pages], free_pages [1]")
+    lib = _native.lib()
+    p = ctypes.byref(pool)
+    ws = _workspace(workspace, lib.kvsel_pages_update_bytes(p, n_out), K)
+    _check(lib.kvsel_pages_update(p, n_in, _i32(table, "table", dev), width, _i32(lens, "lens", dev),
+                                  n_out, _opt(parents, "parents", dev),
+                                  _i32(new_lens, "new_lens", dev), _i32(table_out, "table_out", dev),
+                                  _i32(ref, "ref", dev), _i32(free_pages, "free_pages", dev),
+                                  ws.data_ptr(), ws.nbytes, _raw_stream(dev)), "kvsel_pages_update")
     return table_out, ref, free_pages
 
 
