@@ -479,7 +479,8 @@ int64_t kvsel_paged_attention_bytes(const kvsel_pages* pages, int32_t num_seqs,
  * future query's result does not depend on the order of the rows). Only rows
  * that change their slot are read and written; what lies in slots >= n is
  * left as it is, and kvsel_pages_update then frees their pages. slot_pos
- * [num_layers][keep_rows][H_kv] int32 (or NULL): the row that each slot now holds.
+ * [num_layers][keep_rows][H_kv] int32 (or NULL; not keep_idx's own memory): the row that each
+ * slot now holds.
  * keep_offsets [num_seqs + 1] int32 on the device, nondecreasing from 0.
  * max_keep: an upper bound on n. ref [num_pages] int32 (or NULL: not checked): the
  * references from kvsel_pages_update; a sequence whose slots 0 .. n-1 touch a page with

@@ -6,6 +6,13 @@
 // hole lies before it: no row that is read is written, so the moves need no order at all.
 // That is the least traffic an in-place cut can have: each moved row read once and written
 // once, the others not touched.
+//
+// Bound by memory for a long list, by the plan's chain of loads and barriers for a short one.
+// The plan (who moves where) needs the instance's whole list, so it is made by the block that
+// uses it, in shared memory: a bitmap of the kept rows < n, the movers by a prefix count over
+// the list, the holes by one over the bitmap. Where instances are few, several blocks make the
+// same plan and share out the moves; that costs less than a plan kept in memory and a second
+// launch.
 #include "paged.cuh"
 
 namespace kvsel {
@@ -13,38 +20,54 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 8;            // list entries a thread has in flight
+constexpr int kChunk = 1024;         // moves whose row offsets are in shared memory at a time
+constexpr int kAhead = 4;            // 16-byte vectors a thread moves at a time, of K and of V
 
-// Exclusive prefix of `v` over the block's threads; *total gets the sum.
-__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
+// Prefix count of flags over kBatch rounds of the block's threads, round-major (thread t of round
+// i comes before thread 0 of round i + 1): before[i] gets the flags before this thread's, the
+// return value is their number.
+__device__ __forceinline__ int batch_prefix(const bool (&flag)[kBatch], int (&before)[kBatch],
+                                            int (*counts)[kWarps]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  static_assert(kBatch * kWarps == 64, "two counts a lane");
+  uint32_t mask[kBatch];
+  __syncthreads();                   // the counts of the call before have been read
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    mask[i] = __ballot_sync(0xffffffffu, flag[i]);
+    if (lane == 0) counts[i][warp] = __popc(mask[i]);
+  }
+  __syncthreads();
+  const int2 c = reinterpret_cast<const int2*>(&counts[0][0])[lane];
+  int x = c.x + c.y;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, off);
     if (lane >= off) x += y;
   }
-  __syncthreads();                       // the sums of the call before have been read
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
+  for (int i = 0; i < kBatch; ++i) {
+    const int at = i * kWarps + warp;                          // this warp's count, among the 64
+    const int upto = __shfl_sync(0xffffffffu, x, at >> 1);     // inclusive of the pair
+    const int pair_y = __shfl_sync(0xffffffffu, c.y, at >> 1);
+    const int own = __popc(mask[i]);
+    before[i] = upto - (at & 1 ? own : own + pair_y) + __popc(mask[i] & ((1u << lane) - 1));
   }
-  *total = all;
-  return before + x - v;
+  return __shfl_sync(0xffffffffu, x, 31);
 }
 
-// One block per (layer, sequence, head). Shared: the bitmap of kept rows < n, the movers'
+// Blocks (layer, sequence, head) x parts. Shared: the bitmap of kept rows < n, the movers'
 // list entries and the holes' slots (16 bits each: max_keep <= 32768).
-__global__ void __launch_bounds__(kThreads) paged_compact_kernel(const __grid_constant__ PagedCompactArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) paged_compact_kernel(const __grid_constant__ PagedCompactArgs a,
+                                                                    int parts) {
   extern __shared__ uint32_t smem[];
-  __shared__ int warp_sums[kWarps];
+  __shared__ __align__(8) int counts[kBatch][kWarps];
+  __shared__ uint32_t from[kChunk], to[kChunk];
   __shared__ int bad;
   const int tid = threadIdx.x;
-  const int64_t inst = blockIdx.x;
+  const int64_t inst = blockIdx.x / parts;
+  const int part = (int)(blockIdx.x - inst * parts);
   const int h = (int)(inst % a.pv.Hkv);
   const int b = (int)(inst / a.pv.Hkv % a.S), layer = (int)(inst / a.pv.Hkv / a.S);
   const int max_rows = a.table_width << a.pv.page_shift;
@@ -66,8 +89,9 @@ __global__ void __launch_bounds__(kThreads) paged_compact_kernel(const __grid_co
   if (n < len) {
     for (int col = tid; col < (n + a.pv.page_size - 1) >> a.pv.page_shift; col += kThreads) {
       const int page = checked_page(a.pv, trow, col, a.status);
-      if (page < 0) bad = 1;
-      else if (a.ref && a.ref[page] > 1) {
+      if (page < 0) {
+        bad = 1;
+      } else if (a.ref && a.ref[page] > 1) {
         record_status(a.status, KVSEL_ERR_SHARED_PAGE);
         bad = 1;
       }
@@ -75,77 +99,119 @@ __global__ void __launch_bounds__(kThreads) paged_compact_kernel(const __grid_co
   }
   const int32_t* list = a.keep_idx + ((int64_t)layer * a.keep_rows + o0) * a.pv.Hkv + h;
   int movers = 0;
-  for (int s0 = 0; s0 < n; s0 += kThreads) {
-    const int s = s0 + tid;
-    int idx = 0;
-    bool late = false;
-    if (s < n) {
-      idx = list[(int64_t)s * a.pv.Hkv];
-      late = idx >= n;
-      if (idx < 0 || idx >= len) {
+  for (int s0 = 0; s0 < n; s0 += kThreads * kBatch) {
+    int idx[kBatch], at[kBatch];
+    bool late[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int s = s0 + i * kThreads + tid;
+      idx[i] = s < n ? list[(int64_t)s * a.pv.Hkv] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int s = s0 + i * kThreads + tid;
+      late[i] = s < n && idx[i] >= n;
+      if (s >= n) continue;
+      if (idx[i] < 0 || idx[i] >= len) {
         bad = 1;
         record_status(a.status, KVSEL_ERR_BAD_INDEX);
-      } else if (late) {
-        if (checked_page(a.pv, trow, idx >> a.pv.page_shift, a.status) < 0) bad = 1;
-      } else if (atomicOr(&kept[idx >> 5], 1u << (idx & 31)) >> (idx & 31) & 1u) {
+      } else if (!late[i] && (atomicOr(&kept[idx[i] >> 5], 1u << (idx[i] & 31)) >> (idx[i] & 31) & 1u)) {
         bad = 1;                         // named twice
         record_status(a.status, KVSEL_ERR_BAD_INDEX);
       }
     }
-    int total;
-    const int at = movers + block_prefix(late, warp_sums, &total);
-    if (late) mover[at] = (uint16_t)s;
+    const int total = batch_prefix(late, at, counts);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (late[i]) mover[movers + at[i]] = (uint16_t)(s0 + i * kThreads + tid);
     movers += total;
   }
+  __syncthreads();                       // the bitmap is whole
   int holes = 0;
-  for (int w0 = 0; w0 < words; w0 += kThreads) {
-    const int w = w0 + tid;
-    uint32_t free = 0;
-    if (w < words) {
-      free = ~kept[w];
-      if (w == words - 1 && (n & 31)) free &= (1u << (n & 31)) - 1;
+  for (int s0 = 0; s0 < n; s0 += kThreads * kBatch) {
+    int at[kBatch];
+    bool gap[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int s = s0 + i * kThreads + tid;
+      gap[i] = s < n && !(kept[s >> 5] >> (s & 31) & 1u);
     }
-    int total;
-    int at = holes + block_prefix(__popc(free), warp_sums, &total);
-    while (free) {
-      hole[at++] = (uint16_t)(w * 32 + __ffs(free) - 1);
-      free &= free - 1;
-    }
+    const int total = batch_prefix(gap, at, counts);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (gap[i]) hole[holes + at[i]] = (uint16_t)(s0 + i * kThreads + tid);
     holes += total;
   }
+  // a mover's page out of range: every part has to know, so every part looks at all movers
+  for (int i = tid; i < movers; i += kThreads)
+    if (checked_page(a.pv, trow, list[(int64_t)mover[i] * a.pv.Hkv] >> a.pv.page_shift, a.status) < 0)
+      bad = 1;
   __syncthreads();
-  if (bad) return;                       // uniform: set before the barriers above
+  if (bad) return;                       // uniform; holes == movers from here on
   int32_t* pos = a.slot_pos ? a.slot_pos + ((int64_t)layer * a.keep_rows + o0) * a.pv.Hkv + h : nullptr;
   if (pos)
-    for (int s = tid; s < n; s += kThreads)
+    for (int s = part * kThreads + tid; s < n; s += parts * kThreads)
       if (kept[s >> 5] >> (s & 31) & 1u) pos[(int64_t)s * a.pv.Hkv] = s;
-  const int vecs = a.pv.head_units * 2;  // 16-byte vectors of a head's row
+
+  const int vec_shift = a.pv.head_units == 16 ? 5 : a.pv.head_units == 8 ? 4 : 3;  // vectors of a head
   const int64_t base = layer * a.pv.layer_bytes + (int64_t)h * a.pv.head_units * kRowUnit;
-  for (int e = tid; e < holes * vecs; e += kThreads) {
-    const int i = e / vecs, v = e - i * vecs;
-    const int slot = hole[i], row = list[(int64_t)mover[i] * a.pv.Hkv];
-    const int sp = trow[row >> a.pv.page_shift], dp = trow[slot >> a.pv.page_shift];
-    const int64_t so = base + (int64_t)row_units(a.pv, sp, row & (a.pv.page_size - 1)) * kRowUnit + v * 16;
-    const int64_t d0 = base + (int64_t)row_units(a.pv, dp, slot & (a.pv.page_size - 1)) * kRowUnit + v * 16;
-    *reinterpret_cast<uint4*>(a.pv.k + d0) = *reinterpret_cast<const uint4*>(a.pv.k + so);
-    *reinterpret_cast<uint4*>(a.pv.v + d0) = *reinterpret_cast<const uint4*>(a.pv.v + so);
-    if (pos && v == 0) pos[(int64_t)slot * a.pv.Hkv] = row;
+  char* kb = a.pv.k + base;
+  char* vb = a.pv.v + base;
+  const int m0 = (int)((int64_t)holes * part / parts), m1 = (int)((int64_t)holes * (part + 1) / parts);
+  for (int c0 = m0; c0 < m1; c0 += kChunk) {
+    const int c = min(kChunk, m1 - c0);
+    for (int i = tid; i < c; i += kThreads) {
+      const int slot = hole[c0 + i], row = list[(int64_t)mover[c0 + i] * a.pv.Hkv];
+      from[i] = row_units(a.pv, trow[row >> a.pv.page_shift], row & (a.pv.page_size - 1));
+      to[i] = row_units(a.pv, trow[slot >> a.pv.page_shift], slot & (a.pv.page_size - 1));
+      if (pos) pos[(int64_t)slot * a.pv.Hkv] = row;
+    }
+    __syncthreads();
+    const int vecs = c << vec_shift;
+    for (int e0 = tid; e0 < vecs; e0 += kThreads * kAhead) {
+      uint4 k[kAhead], v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int e = e0 + u * kThreads;
+        if (e < vecs) {
+          const int64_t off = (int64_t)from[e >> vec_shift] * kRowUnit + (e & ((1 << vec_shift) - 1)) * 16;
+          k[u] = __ldcs(reinterpret_cast<const uint4*>(kb + off));
+          v[u] = __ldcs(reinterpret_cast<const uint4*>(vb + off));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int e = e0 + u * kThreads;
+        if (e < vecs) {
+          const int64_t off = (int64_t)to[e >> vec_shift] * kRowUnit + (e & ((1 << vec_shift) - 1)) * 16;
+          *reinterpret_cast<uint4*>(kb + off) = k[u];
+          *reinterpret_cast<uint4*>(vb + off) = v[u];
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_compact(const PagedCompactArgs& a) {
+  static_assert((kMaxKeep / 32) * 4 + 4 * kMaxKeep + 2 * kChunk * 4 + 1024 <= 227 * 1024,
+                "lists and offsets fit shared memory");
   auto lists = [](int n) { return ((n + 31) >> 5) * 4 + 2 * ((n + 1) & ~1) * 2; };
   const int smem = lists(a.max_keep);
-  if (smem > 48 * 1024) {
+  if (smem > 32 * 1024) {
     // always the same value: another thread's call may come between
     const cudaError_t e = cudaFuncSetAttribute(
         paged_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lists(kMaxKeep));
     if (e) return e;
   }
+  // blocks an instance: four an SM in all, with 256 kept rows or more each
   const int64_t insts = (int64_t)a.pv.layers * a.S * a.pv.Hkv;
-  paged_compact_kernel<<<(unsigned)insts, kThreads, smem, a.stream>>>(a);
+  int64_t parts = 4 * (int64_t)a.sm_count / insts;
+  if (parts > (a.max_keep + 255) / 256) parts = (a.max_keep + 255) / 256;
+  if (parts < 1) parts = 1;
+  paged_compact_kernel<<<(unsigned)(insts * parts), kThreads, smem, a.stream>>>(a, (int)parts);
   return cudaGetLastError();
 }
 
