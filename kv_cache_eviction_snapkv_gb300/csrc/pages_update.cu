@@ -7,54 +7,61 @@
 // is 0 and is copied for the others; the pages with count 0 after that are free and go out,
 // lowest first, in the order of (sequence, column). A page that is copied from always keeps
 // a holder, so it is never handed out in the same step.
+//
+// Bound by latency: tables of some 100 KB and one count a page, but four dependent passes over
+// them. So one cluster of eight blocks makes the tables in one launch, with the cluster's
+// hardware barrier between the passes and the blocks' totals in each other's shared memory; a
+// second, dependent launch copies the started pages' rows with the whole machine.
+#include <cooperative_groups.h>
+
 #include "paged.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kvsel {
 namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBlocks = 8;                 // of the cluster
+constexpr int kColumns = 128;              // table columns a warp takes at a time
+constexpr int kPiece = 16384;              // bytes a block copies at a time
 
-// Workspace: owner [num_pages], free list [num_pages], first fresh rank [num_out + 1], and one
-// copy (source page, target page, rows) a sequence.
+// What new sequence b continues: its parent's table row (-1: none), the rows taken over and the
+// rows it ends up with.
+struct Taken {
+  int row, rows, want;
+  int fresh_base;            // rank of its first fresh page; the top bit: its started page stays
+};
+
+// Workspace: Taken [num_out]; copies (source page, target page, rows) [num_out]; owner [num_pages];
+// the blocks' lists of free pages [num_pages]; the number of copies.
 struct Layout {
-  int64_t owner, list, base, copies, bytes;
+  int64_t copies, owner, list, count, bytes;
 };
 __host__ __device__ inline Layout layout_of(int num_pages, int num_out) {
   Layout l;
-  l.copies = 0;
-  l.owner = 16 * (int64_t)num_out;
+  l.copies = 16 * (int64_t)num_out;
+  l.owner = l.copies + 16 * (int64_t)num_out;
   l.list = l.owner + 4 * (int64_t)num_pages;
-  l.base = l.list + 4 * (int64_t)num_pages;
-  l.bytes = l.base + 4 * ((int64_t)num_out + 1);
-  l.bytes = (l.bytes + 15) & ~int64_t(15);
+  l.count = l.list + 4 * (int64_t)num_pages;
+  l.bytes = (l.count + 4 + 15) & ~int64_t(15);
   return l;
 }
 
-// What new sequence b continues: its parent's table row, the rows taken over and the rows it
-// ends up with. A bad parent or length empties it.
-struct Taken {
-  const int32_t* row;
-  int rows, want;
-};
+// A bad parent or length empties the sequence.
 __device__ __forceinline__ Taken taken(const PagesUpdateArgs& a, int b) {
   const int max_rows = a.table_width << a.pv.page_shift;
   const int p = a.parents ? a.parents[b] : b;
-  Taken t{nullptr, 0, a.new_lens[b]};
-  if (p < -1 || p >= a.num_in || t.want < 0 || t.want > max_rows) {
+  Taken t{-1, 0, a.new_lens[b], 0};
+  const int len = p >= 0 && p < a.num_in ? a.lens[p] : 0;
+  if (p < -1 || p >= a.num_in || t.want < 0 || t.want > max_rows || len < 0 || len > max_rows) {
     record_status(a.status, KVSEL_ERR_BAD_INDEX);
     t.want = 0;
-    return t;
+  } else if (p >= 0) {
+    t.row = p;
+    t.rows = min(len, t.want);
   }
-  if (p < 0) return t;
-  const int len = a.lens[p];
-  if (len < 0 || len > max_rows) {
-    record_status(a.status, KVSEL_ERR_BAD_INDEX);
-    t.want = 0;
-    return t;
-  }
-  t.row = a.table + (int64_t)p * a.table_width;
-  t.rows = min(len, t.want);
   return t;
 }
 
@@ -69,116 +76,197 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
   __syncthreads();                       // the sums of the call before have been read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int before = 0, all = 0;
+  int s = warp_sums[lane];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += y;
   }
-  *total = all;
-  return before + x - v;
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  const int before = __shfl_sync(0xffffffffu, s, warp ? warp - 1 : 0);
+  return (warp ? before : 0) + x - v;
 }
 
-__global__ void __launch_bounds__(kThreads) pages_table_kernel(const __grid_constant__ PagesUpdateArgs a) {
+__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
+    pages_table_kernel(const __grid_constant__ PagesUpdateArgs a) {
   __shared__ int warp_sums[kWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int shift = a.pv.page_shift, mask = a.pv.page_size - 1;
-  const Layout lo = layout_of(a.pv.num_pages, a.num_out);
-  int* owner = reinterpret_cast<int*>(a.ws + lo.owner);
-  int* list = reinterpret_cast<int*>(a.ws + lo.list);
-  int* base = reinterpret_cast<int*>(a.ws + lo.base);
-  int4* copies = reinterpret_cast<int4*>(a.ws + lo.copies);
-  for (int p = tid; p < a.pv.num_pages; p += kThreads) {
+  __shared__ int demand_of[kBlocks], free_of[kBlocks];   // every block's, written by their owners
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int gtid = rank * kThreads + tid, gwarp = gtid >> 5;
+  constexpr int kAll = kBlocks * kThreads;
+  const int shift = a.pv.page_shift, mask = a.pv.page_size - 1, P = a.pv.num_pages;
+  const Layout lo = layout_of(P, a.num_out);
+  Taken* const take = reinterpret_cast<Taken*>(a.ws);
+  int4* const copies = reinterpret_cast<int4*>(a.ws + lo.copies);
+  int* const owner = reinterpret_cast<int*>(a.ws + lo.owner);
+  int* const list = reinterpret_cast<int*>(a.ws + lo.list);
+  int* const n_copies = reinterpret_cast<int*>(a.ws + lo.count);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  for (int p = gtid; p < P; p += kAll) {
     a.ref[p] = 0;
     owner[p] = 0x7fffffff;
   }
-  __syncthreads();
+  for (int b = gtid; b < a.num_out; b += kAll) take[b] = taken(a, b);
+  if (gtid == 0) *n_copies = 0;
+  cluster.sync();
+
   // whole uses, and the lowest user of every started page
-  for (int b = warp; b < a.num_out; b += kWarps) {
-    const Taken t = taken(a, b);
-    for (int i = lane; i < t.rows >> shift; i += 32) {
-      const int page = checked_page(a.pv, t.row, i, a.status);
-      if (page >= 0) atomicAdd(&a.ref[page], 1);
-    }
-    if (lane == 0 && (t.rows & mask)) {
-      const int page = checked_page(a.pv, t.row, t.rows >> shift, a.status);
-      if (page >= 0) atomicMin(&owner[page], b);
+  const int chunks = (a.table_width + kColumns - 1) / kColumns;
+  const int64_t items = (int64_t)a.num_out * chunks;
+  for (int64_t it = gwarp; it < items; it += kAll / 32) {
+    const int b = (int)(it / chunks), c0 = (int)(it - (int64_t)b * chunks) * kColumns;
+    const Taken t = take[b];
+    const int whole = t.rows >> shift;
+    if (c0 > whole || t.row < 0) continue;
+    const int32_t* row = a.table + (int64_t)t.row * a.table_width;
+#pragma unroll
+    for (int i = 0; i < kColumns / 32; ++i) {
+      const int col = c0 + lane + 32 * i;
+      if (col < whole) {
+        const int page = checked_page(a.pv, row, col, a.status);
+        if (page >= 0) atomicAdd(&a.ref[page], 1);
+      } else if (col == whole && (t.rows & mask)) {
+        const int page = checked_page(a.pv, row, col, a.status);
+        if (page >= 0) atomicMin(&owner[page], b);
+      }
     }
   }
-  __syncthreads();
-  // who keeps its started page; first fresh rank of every sequence
+  cluster.sync();
+
+  // who keeps its started page; the fresh pages' ranks within this block's run of sequences
+  const int b_run = (a.num_out + kBlocks - 1) / kBlocks;
+  const int b0 = min(a.num_out, rank * b_run), b1 = min(a.num_out, b0 + b_run);
   int demand = 0;
-  for (int b0 = 0; b0 < a.num_out; b0 += kThreads) {
-    const int b = b0 + tid;
+  for (int bb = b0; bb < b1; bb += kThreads) {
+    const int b = bb + tid;
     int fresh = 0;
-    if (b < a.num_out) {
-      const Taken t = taken(a, b);
-      bool keeps = false;
+    Taken t;
+    bool keeps = false;
+    if (b < b1) {
+      t = take[b];
       int src = -1;
       if (t.rows & mask) {
-        src = checked_page(a.pv, t.row, t.rows >> shift, a.status);
+        src = checked_page(a.pv, a.table + (int64_t)t.row * a.table_width, t.rows >> shift, a.status);
         keeps = src >= 0 && a.ref[src] == 0 && owner[src] == b;   // only its owner changes it here
         if (keeps) a.ref[src] = 1;
       }
       fresh = ((t.want + mask) >> shift) - (t.rows >> shift) - (keeps ? 1 : 0);
-      copies[b] = make_int4(keeps ? -1 : src, -1, t.rows & mask, keeps ? 1 : 0);
     }
     int total;
     const int at = block_prefix(fresh, warp_sums, &total);
-    if (b < a.num_out) base[b] = demand + at;
+    if (b < b1) take[b].fresh_base = (demand + at) | (keeps ? (int)0x80000000 : 0);
     demand += total;
   }
-  // the free pages, ascending
+  if (tid < kBlocks) *cluster.map_shared_rank(&demand_of[rank], tid) = demand;
+  cluster.sync();
+
+  // free pages, ascending: a list for every block's run of pages, no longer than the demand
+  int wanted = 0, earlier = 0;
+#pragma unroll
+  for (int r = 0; r < kBlocks; ++r) {
+    wanted += demand_of[r];
+    if (r < rank) earlier += demand_of[r];
+  }
+  const int p_run = (P + kBlocks - 1) / kBlocks;
+  const int p0 = (int)min((int64_t)P, (int64_t)rank * p_run), p1 = min(P, p0 + p_run);
   int nfree = 0;
-  for (int p0 = 0; p0 < a.pv.num_pages; p0 += kThreads) {
-    const int p = p0 + tid;
-    const bool f = p < a.pv.num_pages && a.ref[p] == 0;
+  for (int pp = p0; pp < p1; pp += 4 * kThreads) {
+    bool f[4];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = pp + tid * 4 + i;
+      f[i] = p < p1 && a.ref[p] == 0;
+      n += f[i];
+    }
     int total;
-    const int at = block_prefix(f, warp_sums, &total);
-    if (f) list[nfree + at] = p;
+    int at = nfree + block_prefix(n, warp_sums, &total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (f[i]) {
+        if (at < wanted) list[p0 + at] = pp + tid * 4 + i;
+        ++at;
+      }
     nfree += total;
   }
-  __syncthreads();
-  if (tid == 0) {
-    if (a.free_pages) *a.free_pages = nfree - demand;
-    if (demand > nfree) record_status(a.status, KVSEL_ERR_NO_PAGES);
+  if (tid < kBlocks) *cluster.map_shared_rank(&free_of[rank], tid) = nfree;
+  cluster.sync();
+
+  int all_free = 0;
+#pragma unroll
+  for (int r = 0; r < kBlocks; ++r) all_free += free_of[r];
+  if (gtid == 0) {
+    if (a.free_pages) *a.free_pages = all_free - wanted;
+    if (wanted > all_free) record_status(a.status, KVSEL_ERR_NO_PAGES);
   }
-  for (int b = warp; b < a.num_out; b += kWarps) {
-    const Taken t = taken(a, b);
-    const int4 c = copies[b];
-    const int whole = t.rows >> shift, held = whole + c.w, need = (t.want + mask) >> shift;
+  for (int64_t it = gwarp; it < items; it += kAll / 32) {
+    const int b = (int)(it / chunks), c0 = (int)(it - (int64_t)b * chunks) * kColumns;
+    const Taken t = take[b];
+    int base = t.fresh_base & 0x7fffffff;
+    for (int r = 0; r < b / b_run; ++r) base += demand_of[r];
+    const int whole = t.rows >> shift, held = whole + (t.fresh_base < 0 ? 1 : 0);
+    const int need = (t.want + mask) >> shift;
+    const int32_t* row = a.table + (int64_t)t.row * a.table_width;
     int32_t* out = a.table_out + (int64_t)b * a.table_width;
-    for (int i = lane; i < a.table_width; i += 32) {
+#pragma unroll
+    for (int i = 0; i < kColumns / 32; ++i) {
+      const int col = c0 + lane + 32 * i;
+      if (col >= a.table_width) continue;
       int page = -1;
-      if (i < held) {
-        page = checked_page(a.pv, t.row, i, a.status);
-      } else if (i < need) {
-        const int rank = base[b] + i - held;
-        if (rank < nfree) {
-          page = list[rank];
+      if (col < held) {
+        page = checked_page(a.pv, row, col, a.status);
+      } else if (col < need) {
+        int k = base + col - held;                       // its rank among the free pages
+        if (k < all_free) {
+          int r = 0;
+          while (k >= free_of[r]) k -= free_of[r++];
+          page = list[(int64_t)r * p_run + k];
           a.ref[page] = 1;
-          if (i == whole && c.z) copies[b].y = page;
+          if (col == whole && (t.rows & mask)) {
+            const int src = checked_page(a.pv, row, col, a.status);
+            if (src >= 0) copies[atomicAdd(n_copies, 1)] = make_int4(src, page, t.rows & mask, 0);
+          }
         }
       }
-      out[i] = page;
+      out[col] = page;
     }
   }
+  cluster.sync();            // no block leaves while another reads its shared memory
 }
 
-// Rows of started pages for their new holders: one block per (sequence, layer).
+// Rows of started pages for their new holders, in pieces of kPiece bytes: (copy, layer, K or V,
+// piece). The copies' order does not matter: no target is a source or another's target.
 __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__ PagesUpdateArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Layout lo = layout_of(a.pv.num_pages, a.num_out);
-  const int b = blockIdx.x;
-  const int4 c = reinterpret_cast<const int4*>(a.ws + lo.copies)[b];
-  if (c.x < 0 || c.y < 0) return;
-  const int64_t base = (int64_t)blockIdx.y * a.pv.layer_bytes;
-  const int64_t so = base + (int64_t)row_units(a.pv, c.x, 0) * kRowUnit;
-  const int64_t d0 = base + (int64_t)row_units(a.pv, c.y, 0) * kRowUnit;
-  const int64_t vecs = (int64_t)c.z * a.pv.row_units * 2;
-  for (int64_t e = threadIdx.x; e < vecs; e += blockDim.x) {
-    *reinterpret_cast<uint4*>(a.pv.k + d0 + e * 16) = *reinterpret_cast<const uint4*>(a.pv.k + so + e * 16);
-    *reinterpret_cast<uint4*>(a.pv.v + d0 + e * 16) = *reinterpret_cast<const uint4*>(a.pv.v + so + e * 16);
+  const int n = *reinterpret_cast<const int*>(a.ws + lo.count);
+  const int64_t row_bytes = (int64_t)a.pv.row_units * kRowUnit;
+  const int pieces = (int)((row_bytes * (a.pv.page_size - 1) + kPiece - 1) / kPiece);
+  const int64_t items = (int64_t)n * a.pv.layers * 2 * pieces;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t rest = it / pieces;
+    const int64_t from = (it - rest * pieces) * kPiece;
+    const int64_t cl = rest >> 1;
+    const int layer = (int)(cl % a.pv.layers);
+    const int4 c = reinterpret_cast<const int4*>(a.ws + lo.copies)[cl / a.pv.layers];
+    const int64_t bytes = min((int64_t)kPiece, c.z * row_bytes - from);
+    char* base = (rest & 1 ? a.pv.v : a.pv.k) + layer * a.pv.layer_bytes + from;
+    const char* src = base + (int64_t)row_units(a.pv, c.x, 0) * kRowUnit;
+    char* dst = base + (int64_t)row_units(a.pv, c.y, 0) * kRowUnit;
+    uint4 v[kPiece / 4096];
+#pragma unroll
+    for (int i = 0; i < kPiece / 4096; ++i) {
+      const int e = (i * 256 + threadIdx.x) * 16;
+      if (e < bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + e));
+    }
+#pragma unroll
+    for (int i = 0; i < kPiece / 4096; ++i) {
+      const int e = (i * 256 + threadIdx.x) * 16;
+      if (e < bytes) *reinterpret_cast<uint4*>(dst + e) = v[i];
+    }
   }
 }
 
@@ -187,11 +275,23 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__
 int64_t pages_update_ws(int num_pages, int num_out) { return layout_of(num_pages, num_out).bytes; }
 
 cudaError_t launch_pages_update(const PagesUpdateArgs& a) {
-  pages_table_kernel<<<1, kThreads, 0, a.stream>>>(a);
+  pages_table_kernel<<<kBlocks, kThreads, 0, a.stream>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e || a.num_out == 0 || a.pv.num_pages == 0) return e;
-  pages_copy_kernel<<<dim3((unsigned)a.num_out, (unsigned)a.pv.layers), 256, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  // pages of one row are never started
+  if (e || a.num_out == 0 || a.pv.num_pages == 0 || a.pv.page_size == 1) return e;
+  cudaLaunchConfig_t cfg{};
+  // as many blocks as there can be pieces, or as the SMs hold at a time
+  const int64_t pieces = ((int64_t)a.pv.row_units * kRowUnit * (a.pv.page_size - 1) + kPiece - 1) / kPiece;
+  const int64_t most = (int64_t)a.num_out * a.pv.layers * 2 * pieces;
+  cfg.gridDim = dim3((unsigned)(most < 8 * (int64_t)a.sm_count ? most : 8 * (int64_t)a.sm_count));
+  cfg.blockDim = dim3(256);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pages_copy_kernel, a);
 }
 
 }  // namespace kvsel
