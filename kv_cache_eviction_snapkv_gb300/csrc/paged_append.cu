@@ -92,11 +92,12 @@ __device__ __forceinline__ int64_t target_row(const AppendArgs& a, int n) {
 // A warp takes `per_warp` passes of one (layer, token); a pass is 32 / kLanes heads of one
 // kind: all of q's passes, then k's, then v's.
 template <typename T, int kLanes>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a,
-                                                          int per_warp) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a,
+                                                             int per_warp) {
   constexpr int E = 16 / sizeof(T);               // elements a lane holds of a head
   constexpr int D = kLanes * E, kHeads = 32 / kLanes, kRowBytes = kLanes * 16;
   constexpr int kAhead = 4;                       // passes whose loads go out together
+  __shared__ float turn[2 * E][kThreads];         // every lane's own cosines and sines
   const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
   const int hk = a.src[1] ? a.pv.Hkv : 0;
   const int pq = (a.H + kHeads - 1) / kHeads, pk = (hk + kHeads - 1) / kHeads;
@@ -133,27 +134,23 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const bool turns = e0 < a.rot;
   const bool cross = turns && !a.interleaved;     // the other elements are in another lane
   const int other_lane = cross ? lane + (e0 < half ? half : -half) / E : lane;
-  float c[E], s[E], wa[E], wb[E];
+  float wa[E], wb[E];
   if (turns && p0 < pq + pk) {
     const int position = a.positions[n];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      if (a.interleaved) {
-        if (i % 2 == 0) rotation(position, a.inv_freq[(e0 + i) / 2], a.rope_scale, &c[i], &s[i]);
-        else c[i] = c[i - 1], s[i] = s[i - 1];
-      } else {
-        rotation(position, a.inv_freq[e0 < half ? e0 + i : e0 + i - half], a.rope_scale, &c[i], &s[i]);
-      }
+      const int e = e0 + i;
+      const int pair = a.interleaved ? e >> 1 : e < half ? e : e - half;
+      float c, s;
+      rotation(position, a.inv_freq[pair], a.rope_scale, &c, &s);
+      turn[i][threadIdx.x] = c;
+      turn[E + i][threadIdx.x] = (a.interleaved ? i % 2 == 0 : e < half) ? -s : s;
     }
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (a.interleaved ? i % 2 == 0 : e0 < half) s[i] = -s[i];
   }
 
   int have = -1;                                  // kind that wa, wb are for
   for (int p = p0; p < p1; p += kAhead) {
-    uint4 ahead[kAhead];
-    load(ahead, p + kAhead);
+    if (p > p0) load(v, p);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (p + u >= p1) break;
@@ -177,8 +174,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 #pragma unroll
           for (int i = 0; i < E; ++i) {
             const float away = __shfl_sync(0xffffffffu, w[i], other_lane);
-            wa[i] = turns ? w[i] * c[i] : w[i];
-            wb[i] = turns ? (cross ? away : w[i ^ 1]) * s[i] : 0.f;
+            wa[i] = turns ? w[i] * turn[i][threadIdx.x] : w[i];
+            wb[i] = turns ? (cross ? away : w[i ^ 1]) * turn[E + i][threadIdx.x] : 0.f;
           }
         }
         float x[E], o[E];
@@ -213,8 +210,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       }
       if (live && (kind == 0 || row >= 0)) *reinterpret_cast<uint4*>(dst + sub * 16) = y;
     }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) v[u] = ahead[u];
   }
 }
 

@@ -28,7 +28,13 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;                    // rows of a step
-constexpr int kJoinThreads = 512;
+// What an instance's start and end cost, in steps: 48 sequences of 1 to 8192 rows took 77 us
+// with 0, 49 with 1, 42.7 with 2, 42.5 with 3.
+constexpr int kSegment = 2;
+// Units that are worth a part of their own: one sequence of 293 rows took 9.7 us with 4, 8.1
+// with 2.
+constexpr int kLeast = 2;
+constexpr int kJoinThreads = 256;
 
 // What the launch fixes; the rest follows from the lengths.
 struct AttnGeom {
@@ -142,17 +148,27 @@ struct Step {
   }
 
   // q in the order of K's pieces; heads past the group's are zero
-  __device__ __forceinline__ void begin(const char* q, int n_heads, int lane) {
+  struct Query {
+    uint4 w[NT][kKw / 4];
+  };
+  static __device__ __forceinline__ void fetch(Query& f, const char* q, int n_heads, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      const int h = x * 8 + g;
+    for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int c = 0; c < kKw / 4; ++c) {             // 16 bytes at a time
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (h < n_heads)
-          w = *reinterpret_cast<const uint4*>(q + (int64_t)h * kRowBytes + (c >> 1) * 128 + t * 32 +
-                                              (c & 1) * 16);
+        f.w[x][c] = make_uint4(0, 0, 0, 0);
+        if (x * 8 + g < n_heads)
+          f.w[x][c] = *reinterpret_cast<const uint4*>(q + (int64_t)(x * 8 + g) * kRowBytes +
+                                                      (c >> 1) * 128 + t * 32 + (c & 1) * 16);
+      }
+  }
+  __device__ __forceinline__ void begin(const Query& f) {
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+#pragma unroll
+      for (int c = 0; c < kKw / 4; ++c) {
+        const uint4 w = f.w[x][c];
         if constexpr (kEb == 2) {
           qf[x][4 * c] = w.x;
           qf[x][4 * c + 1] = w.y;
@@ -342,14 +358,17 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (St::kStages * St::kStage);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // steps before every sequence
+  // units before every sequence: its steps, and kSegment more that stand for an instance's start
+  // and end (a part of many short instances would take far longer than one of a long one)
   const int max_rows = a.table_width << a.pv.page_shift;
   int nb = 0;
   for (int b0 = 0; b0 < a.S; b0 += kThreads) {
     const int b = b0 + tid;
     int x = 0;
-    if (b < a.S)
-      x = (int)(((int64_t)checked_len(a.lens[b], max_rows, a.status) + kRows - 1) / kRows);
+    if (b < a.S) {
+      const int len = checked_len(a.lens[b], max_rows, a.status);
+      x = len ? (int)(((int64_t)len + kRows - 1) / kRows) + kSegment : 0;
+    }
     int y = x;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -386,46 +405,55 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
   const int HH = a.pv.Hkv * gm.HG, warps = gm.grid * kWarps;
   const int64_t per_layer = (int64_t)nb * HH;
   const int64_t units = per_layer * a.pv.layers;
-  const int parts = (int)min((int64_t)warps, units);          // every part has a step at least
+  const int parts = (int)min((int64_t)warps, (units + kLeast - 1) / kLeast);
   const int part = blockIdx.x * kWarps + warp;
   auto part_start = [&](int64_t c) { return quotient(c * units, parts); };
   const bool works = part < parts;
   const int64_t u0 = works ? part_start(part) : 0, u1 = works ? part_start(part + 1) : 0;
 
+  // The instance at unit u of this part, and its steps [first, last) within the part: none where
+  // the part ends before the instance's first step.
   struct Place {
-    int layer, b, head, blk, n_blk;
+    int layer, b, head, first, last, n_steps;
+    int64_t end;              // of the instance, or of the part
   };
   auto locate = [&](int64_t u) {
     Place x;
     x.layer = a.pv.layers == 1 ? 0 : (int)quotient(u, per_layer);
     const int64_t rem = u - x.layer * per_layer;
     x.b = upper_find(a.S, (int)quotient(rem, HH), [&](int i) { return pre[i]; });
-    x.n_blk = pre[x.b + 1] - pre[x.b];
+    const int n = pre[x.b + 1] - pre[x.b];
     const int64_t local = rem - (int64_t)pre[x.b] * HH;
-    x.head = (int)quotient(local, x.n_blk);
-    x.blk = (int)(local - (int64_t)x.head * x.n_blk);
+    x.head = (int)quotient(local, n);
+    const int at = (int)(local - (int64_t)x.head * n);
+    x.end = min(u + (n - at), u1);
+    x.n_steps = n - kSegment;
+    x.first = max(0, at - kSegment);
+    x.last = max(0, at + (int)(x.end - u) - kSegment);
     return x;
   };
 
-  // the copying side: the next step to copy, its instance's rows and this lane's table entry
-  int64_t pu = u0, p_end = u0;
-  int p_row = 0, p_len = 0, p_page = -1;
+  // the copying side: the instance that it is in, and this lane's row and table entry for the
+  // next step to copy
+  int64_t pu = u0;                        // unit after that instance
+  int p_left = 0, p_row = 0, p_len = 0, p_page = -1;
   const int32_t* p_table = nullptr;
   int64_t p_base = 0;
   auto look = [&] {
-    if (pu == p_end) {
+    while (p_left == 0 && pu < u1) {
       const Place x = locate(pu);
-      p_end = pu + min((int64_t)(x.n_blk - x.blk), u1 - pu);
-      p_row = x.blk * kRows + (lane & 15);
+      pu = x.end;
+      p_left = x.last - x.first;
+      p_row = x.first * kRows + (lane & 15);
       p_len = min(max(a.lens[x.b], 0), max_rows);
       p_table = a.table + (int64_t)x.b * a.table_width;
       p_base = x.layer * a.pv.layer_bytes + (int64_t)quotient(x.head, gm.HG) * a.pv.head_units * kRowUnit;
     }
-    p_page = p_row < p_len ? __ldg(p_table + (p_row >> a.pv.page_shift)) : -1;
+    if (p_left) p_page = p_row < p_len ? __ldg(p_table + (p_row >> a.pv.page_shift)) : -1;
   };
   St st;
   auto copy_step = [&](int slot) {
-    if (pu < u1) {
+    if (p_left) {
       const bool in = p_row < p_len;
       const bool ok = in && p_page >= 0 && p_page < a.pv.num_pages;
       if (in && !ok) record_status(a.status, KVSEL_ERR_BAD_INDEX);
@@ -437,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
       if (v) st.issue(ring + slot * St::kStage, a.pv.k + p_base, a.pv.v + p_base, off, lane);
       if (lane == 0) valid[slot] = v;
       p_row += kRows;
-      if (++pu < u1) look();
+      --p_left;
+      look();
     }
     copies_commit();
   };
@@ -446,18 +475,31 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
   float2* const ml = reinterpret_cast<float2*>(a.ws + ws_ml(warps));
   float* const acc = reinterpret_cast<float*>(a.ws + ws_acc(warps, gm.heads));
 
-  if (works) look();
+  look();
 #pragma unroll
   for (int i = 0; i < St::kStages - 1; ++i) copy_step(i);
   int slot = 0;
-  for (int64_t u = u0; u < u1;) {
-    const Place x = locate(u);
-    const int n = (int)min((int64_t)(x.n_blk - x.blk), u1 - u);
+  // the next instance with steps in this part, and its heads' queries
+  Place x{};
+  typename St::Query query;
+  int64_t u = u0, first_head = 0;
+  int n_heads = 0;
+  auto next = [&] {
+    x.first = x.last = 0;
+    while (x.first == x.last && u < u1) {
+      x = locate(u);
+      if (x.first == x.last) u = x.end;
+    }
+    if (x.first == x.last) return;
     const int kvh = (int)quotient(x.head, gm.HG), hg = x.head - kvh * gm.HG;
-    const int n_heads = min(gm.heads, gm.G - hg * gm.heads);
-    const int64_t first_head = ((int64_t)x.layer * a.S + x.b) * a.H + kvh * gm.G + hg * gm.heads;
-    st.begin(static_cast<const char*>(a.q) + first_head * St::kRowBytes, n_heads, lane);
-    for (int i = 0; i < n; ++i) {
+    n_heads = min(gm.heads, gm.G - hg * gm.heads);
+    first_head = ((int64_t)x.layer * a.S + x.b) * a.H + kvh * gm.G + hg * gm.heads;
+    St::fetch(query, static_cast<const char*>(a.q) + first_head * St::kRowBytes, n_heads, lane);
+  };
+  next();
+  while (x.first < x.last) {
+    st.begin(query);
+    for (int i = x.first; i < x.last; ++i) {
       copies_wait<St::kStages - 2>();
       __syncwarp();                    // every lane's copies are there, and the step before is read
       copy_step(slot == 0 ? St::kStages - 1 : slot - 1);
@@ -471,8 +513,21 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
       slot = slot == St::kStages - 1 ? 0 : slot + 1;
     }
 
-    const bool whole = x.blk == 0 && n == x.n_blk;
-    const int64_t at = ((int64_t)part * 2 + (x.blk > 0 ? 0 : 1)) * gm.heads;
+    const bool begins = x.first == 0, whole = begins && x.last == x.n_steps;
+    const int64_t at = ((int64_t)part * 2 + (begins ? 1 : 0)) * gm.heads;
+    const int64_t first = first_head;
+    const int heads = n_heads;
+    if (begins && !whole) {
+      // its last piece is the last part's that starts before its end
+      const int64_t end = x.end + (x.n_steps - x.last);
+      info.first_head = first;
+      info.heads = heads;
+      info.last = (int)min((int64_t)parts - 1, quotient(end * parts, units));
+      while (part_start(info.last) >= end) --info.last;
+      while (info.last + 1 < parts && part_start(info.last + 1) < end) ++info.last;
+    }
+    u = x.end;
+    next();                            // its queries arrive while this one's results go out
     bool bad = false;
 #pragma unroll
     for (int y = 0; y < NT; ++y)
@@ -483,9 +538,9 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         const int h = y * 8 + 2 * t + c;
-        if (h >= n_heads) continue;
+        if (h >= heads) continue;
         const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        float4* to = reinterpret_cast<float4*>((whole ? a.out + (first_head + h) * D : acc + (at + h) * D) +
+        float4* to = reinterpret_cast<float4*>((whole ? a.out + (first + h) * D : acc + (at + h) * D) +
                                                g * (D / 8));
         if (whole) bad |= !finite_f(l);
 #pragma unroll
@@ -497,89 +552,101 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
         }
         if (g == 0 && !whole) ml[at + h] = make_float2(st.m[y][c], l);
         if (g == 0 && whole && a.lse)
-          a.lse[first_head + h] = l == 0.f ? -INFINITY : (st.m[y][c] + log2f(l)) * 0.6931471805599453f;
+          a.lse[first + h] = l == 0.f ? -INFINITY : (st.m[y][c] + log2f(l)) * 0.6931471805599453f;
       }
     if (bad) record_status(a.status, KVSEL_ERR_NONFINITE);
-    if (x.blk == 0 && !whole) {
-      // its last piece is the last part's that starts before its end
-      const int64_t end = u + x.n_blk;
-      info.first_head = first_head;
-      info.heads = n_heads;
-      info.last = (int)min((int64_t)parts - 1, quotient(end * parts, units));
-      while (part_start(info.last) >= end) --info.last;
-      while (info.last + 1 < parts && part_start(info.last + 1) < end) ++info.last;
-    }
-    u += n;
   }
   if (lane == 0) reinterpret_cast<SplitInfo*>(a.ws)[part] = info;
 }
 
-// Joins the pieces of the instances that start in part c and end in a later one: slot 1 of c,
-// then slot 0 of the parts up to `last`. A block's warps share the instance's heads, and the
-// pieces of a head where there are fewer heads than warps.
+// Joins the pieces of the instance that starts in part c and ends in a later one, if there is
+// one: slot 1 of c, then slot 0 of the parts up to `last`. The block's warps share the heads, and
+// the pieces of a head where there are fewer heads than warps; every warp keeps a maximum of its
+// own, so that one round of loads does.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a,
                                                                   const __grid_constant__ AttnGeom gm) {
-  constexpr int kJoinWarps = kJoinThreads / 32, E = D / 32;
-  __shared__ float sums[kJoinWarps], vals[kJoinWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kJoinWarps = kJoinThreads / 32, E = D / 32, kAhead = 8;
+  __shared__ float maxs[kJoinWarps], sums[kJoinWarps], vals[kJoinWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   const int warps = gm.grid * kWarps;
-  int per = kJoinWarps;                       // warps a head: a power of two, heads <= 16
-  while (per * gm.heads > kJoinWarps) per >>= 1;
-  const int h = warp / per, sub = warp - h * per;
+  int per = kJoinWarps;                       // warps a head: a power of two
+  while (per > 1 && per * gm.heads > kJoinWarps) per >>= 1;
+  const int sub = warp & (per - 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float2* ml = reinterpret_cast<const float2*>(a.ws + ws_ml(warps));
   const float* acc = reinterpret_cast<const float*>(a.ws + ws_acc(warps, gm.heads));
-  for (int c = blockIdx.x; c < warps; c += gridDim.x) {
-    const SplitInfo info = reinterpret_cast<const SplitInfo*>(a.ws)[c];
-    if (info.first_head < 0) continue;
-    const int n = info.last - c + 1;
-    auto at = [&](int i) { return ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * gm.heads + h; };
+  const SplitInfo info = reinterpret_cast<const SplitInfo*>(a.ws)[c];
+  if (info.first_head < 0) return;
+  const int n = info.last - c + 1;
+  for (int h0 = 0; h0 < info.heads; h0 += kJoinWarps / per) {
+    const int h = h0 + warp / per;
     float mx = -INFINITY, sum = 0.f, v[E] = {};
     if (h < info.heads) {
-      for (int i = lane; i < n; i += 32) mx = fmaxf(mx, ml[at(i)].x);
+      for (int i0 = sub; i0 < n; i0 += per * kAhead) {
+        float2 y[kAhead];
+        float w[kAhead][E];
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-#pragma unroll 8
-      for (int i = sub; i < n; i += per) {
-        const float2 y = ml[at(i)];
-        const float f = y.x == -INFINITY ? 0.f : ex2(y.x - mx);   // a NaN sum stays NaN
-        sum = fmaf(y.y, f, sum);
-        const float* p = acc + at(i) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 w = *reinterpret_cast<const float4*>(p);
-          v[0] = fmaf(w.x, f, v[0]);
-          v[1] = fmaf(w.y, f, v[1]);
-          v[2] = fmaf(w.z, f, v[2]);
-          v[3] = fmaf(w.w, f, v[3]);
-        } else {
-          const float2 w = *reinterpret_cast<const float2*>(p);
-          v[0] = fmaf(w.x, f, v[0]);
-          v[1] = fmaf(w.y, f, v[1]);
+        for (int k = 0; k < kAhead; ++k) {
+          const int i = i0 + k * per;
+          const int64_t at = ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * gm.heads + h;
+          y[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) w[k][e] = 0.f;
+          if (i < n) {
+            y[k] = ml[at];
+            if constexpr (E == 4)
+              *reinterpret_cast<float4*>(w[k]) = *reinterpret_cast<const float4*>(acc + at * D + lane * E);
+            else
+              *reinterpret_cast<float2*>(w[k]) = *reinterpret_cast<const float2*>(acc + at * D + lane * E);
+          }
+        }
+        float top = mx;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, y[k].x);
+        const float ref = top == -INFINITY ? 0.f : top, f = ex2(mx - ref);
+        mx = top;
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float p = ex2(y[k].x - ref);        // of -inf: 0; a NaN sum stays NaN
+          sum = fmaf(y[k].y, p, sum);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = fmaf(w[k][e], p, v[e]);
         }
       }
     }
-    __syncthreads();                          // the sums of the instance before have been read
-    if (lane == 0) sums[warp] = sum;
+    __syncthreads();                          // the heads before have been read
+    if (lane == 0) {
+      maxs[warp] = mx;
+      sums[warp] = sum;
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) vals[warp][lane * E + e] = v[e];
     __syncthreads();
     if (sub == 0 && h < info.heads) {
-      for (int w = 1; w < per; ++w) {
-        sum += sums[warp + w];
+      float top = mx;
+      for (int w = 1; w < per; ++w) top = fmaxf(top, maxs[warp + w]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float total = 0.f, r[E] = {};
+      for (int w = 0; w < per; ++w) {
+        const float f = ex2(maxs[warp + w] - ref);
+        total = fmaf(sums[warp + w], f, total);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] += vals[warp + w][lane * E + e];
+        for (int e = 0; e < E; ++e) r[e] = fmaf(vals[warp + w][lane * E + e], f, r[e]);
       }
-      bool bad = !finite_f(sum);
+      bool bad = !finite_f(total);
       float* out = a.out + (info.first_head + h) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        v[e] = sum == 0.f ? 0.f : v[e] / sum;
-        bad |= !finite_f(v[e]);
-        out[e] = v[e];
+        r[e] = total == 0.f ? 0.f : r[e] / total;
+        bad |= !finite_f(r[e]);
+        out[e] = r[e];
       }
       if (lane == 0 && a.lse)
-        a.lse[info.first_head + h] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+        a.lse[info.first_head + h] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
       if (bad) record_status(a.status, KVSEL_ERR_NONFINITE);
     }
   }
@@ -618,7 +685,7 @@ cudaError_t launch(const PagedAttnArgs& a, const AttnGeom& gm) {
   paged_attn_kernel<T, D, NT><<<gm.grid, kThreads, smem_bytes<T, D, NT>(a.S), a.stream>>>(a, gm);
   if ((e = cudaGetLastError())) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(gm.grid * kWarps < 4 * a.sm_count ? gm.grid * kWarps : 4 * a.sm_count));
+  cfg.gridDim = dim3((unsigned)(gm.grid * kWarps));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = a.stream;
   cudaLaunchAttribute at[1];

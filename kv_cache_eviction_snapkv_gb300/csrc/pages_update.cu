@@ -24,7 +24,8 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 8;                 // of the cluster
-constexpr int kColumns = 128;              // table columns a warp takes at a time
+constexpr int kAtOnce = 8;                 // table entries a thread has in flight
+constexpr int kTiles = 32;                 // of a page a thread, counted together
 constexpr int kPiece = 16384;              // bytes a block copies at a time
 
 // What new sequence b continues: its parent's table row (-1: none), the rows taken over and the
@@ -65,6 +66,7 @@ __device__ __forceinline__ Taken taken(const PagesUpdateArgs& a, int b) {
   return t;
 }
 
+// Exclusive prefix of `v` over the block's threads.
 __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -89,12 +91,12 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
 
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
     pages_table_kernel(const __grid_constant__ PagesUpdateArgs a) {
-  __shared__ int warp_sums[kWarps];
+  __shared__ int warp_sums[kWarps], tile_sums[kTiles * kWarps];
   __shared__ int demand_of[kBlocks], free_of[kBlocks];   // every block's, written by their owners
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31;
-  const int gtid = rank * kThreads + tid, gwarp = gtid >> 5;
+  const int gtid = rank * kThreads + tid;
   constexpr int kAll = kBlocks * kThreads;
   const int shift = a.pv.page_shift, mask = a.pv.page_size - 1, P = a.pv.num_pages;
   const Layout lo = layout_of(P, a.num_out);
@@ -114,24 +116,23 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
   cluster.sync();
 
   // whole uses, and the lowest user of every started page
-  const int chunks = (a.table_width + kColumns - 1) / kColumns;
-  const int64_t items = (int64_t)a.num_out * chunks;
-  for (int64_t it = gwarp; it < items; it += kAll / 32) {
-    const int b = (int)(it / chunks), c0 = (int)(it - (int64_t)b * chunks) * kColumns;
-    const Taken t = take[b];
-    const int whole = t.rows >> shift;
-    if (c0 > whole || t.row < 0) continue;
-    const int32_t* row = a.table + (int64_t)t.row * a.table_width;
+  const uint32_t W = (uint32_t)a.table_width, entries = (uint32_t)a.num_out * W;
+  for (uint32_t e0 = gtid; e0 < entries; e0 += kAll * kAtOnce) {
+    Taken t[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kColumns / 32; ++i) {
-      const int col = c0 + lane + 32 * i;
-      if (col < whole) {
-        const int page = checked_page(a.pv, row, col, a.status);
-        if (page >= 0) atomicAdd(&a.ref[page], 1);
-      } else if (col == whole && (t.rows & mask)) {
-        const int page = checked_page(a.pv, row, col, a.status);
-        if (page >= 0) atomicMin(&owner[page], b);
-      }
+    for (int i = 0; i < kAtOnce; ++i) {
+      const uint32_t e = e0 + i * kAll;
+      t[i] = take[e < entries ? e / W : 0];
+      t[i].want = e < entries ? (int)(e % W) : a.table_width;    // the column
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int whole = t[i].rows >> shift, col = t[i].want;
+      if (col > whole || (col == whole && !(t[i].rows & mask))) continue;
+      const int page = checked_page(a.pv, a.table + (int64_t)t[i].row * W, col, a.status);
+      if (page < 0) continue;
+      if (col < whole) atomicAdd(&a.ref[page], 1);
+      else atomicMin(&owner[page], (int)((e0 + i * kAll) / W));
     }
   }
   cluster.sync();
@@ -173,24 +174,32 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
   const int p_run = (P + kBlocks - 1) / kBlocks;
   const int p0 = (int)min((int64_t)P, (int64_t)rank * p_run), p1 = min(P, p0 + p_run);
   int nfree = 0;
-  for (int pp = p0; pp < p1; pp += 4 * kThreads) {
-    bool f[4];
-    int n = 0;
+  for (int64_t pp = p0; pp < p1; pp += kTiles * kThreads) {
+    const int tiles = (int)min((int64_t)kTiles, (p1 - pp + kThreads - 1) / kThreads);
+    uint32_t mine = 0;                   // bit i: page pp + 1024 i + thread is free
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = pp + tid * 4 + i;
-      f[i] = p < p1 && a.ref[p] == 0;
-      n += f[i];
+    for (int i = 0; i < kTiles; ++i) {
+      const int64_t p = pp + i * kThreads + tid;
+      if (p < p1 && a.ref[p] == 0) mine |= 1u << i;
     }
+    tile_sums[tid] = 0;
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+      const uint32_t all = __ballot_sync(0xffffffffu, mine >> i & 1u);
+      if (lane == 0) tile_sums[i * kWarps + (tid >> 5)] = __popc(all);
+    }
+    __syncthreads();
     int total;
-    int at = nfree + block_prefix(n, warp_sums, &total);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (f[i]) {
-        if (at < wanted) list[p0 + at] = pp + tid * 4 + i;
-        ++at;
-      }
+    const int before = block_prefix(tile_sums[tid], warp_sums, &total);
+    tile_sums[tid] = nfree + before;
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+      const uint32_t all = __ballot_sync(0xffffffffu, mine >> i & 1u);
+      const int at = tile_sums[i * kWarps + (tid >> 5)] + __popc(all & ((1u << lane) - 1));
+      if ((mine >> i & 1u) && at < wanted) list[p0 + at] = (int)(pp + i * kThreads + tid);
+    }
     nfree += total;
+    __syncthreads();
   }
   if (tid < kBlocks) *cluster.map_shared_rank(&free_of[rank], tid) = nfree;
   cluster.sync();
@@ -202,36 +211,42 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
     if (a.free_pages) *a.free_pages = all_free - wanted;
     if (wanted > all_free) record_status(a.status, KVSEL_ERR_NO_PAGES);
   }
-  for (int64_t it = gwarp; it < items; it += kAll / 32) {
-    const int b = (int)(it / chunks), c0 = (int)(it - (int64_t)b * chunks) * kColumns;
-    const Taken t = take[b];
-    int base = t.fresh_base & 0x7fffffff;
-    for (int r = 0; r < b / b_run; ++r) base += demand_of[r];
-    const int whole = t.rows >> shift, held = whole + (t.fresh_base < 0 ? 1 : 0);
-    const int need = (t.want + mask) >> shift;
-    const int32_t* row = a.table + (int64_t)t.row * a.table_width;
-    int32_t* out = a.table_out + (int64_t)b * a.table_width;
+  for (uint32_t e0 = gtid; e0 < entries; e0 += kAll * kAtOnce) {
+    Taken t[kAtOnce];
+    int col[kAtOnce], page[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kColumns / 32; ++i) {
-      const int col = c0 + lane + 32 * i;
-      if (col >= a.table_width) continue;
-      int page = -1;
-      if (col < held) {
-        page = checked_page(a.pv, row, col, a.status);
-      } else if (col < need) {
-        int k = base + col - held;                       // its rank among the free pages
+    for (int i = 0; i < kAtOnce; ++i) {
+      const uint32_t e = e0 + i * kAll;
+      col[i] = e < entries ? (int)(e % W) : -1;
+      t[i] = take[col[i] < 0 ? 0 : e / W];
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int held = (t[i].rows >> shift) + (t[i].fresh_base < 0 ? 1 : 0);
+      page[i] = -1;
+      if (col[i] >= 0 && col[i] < held)
+        page[i] = checked_page(a.pv, a.table + (int64_t)t[i].row * W, col[i], a.status);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (col[i] < 0) continue;
+      const uint32_t e = e0 + i * kAll;
+      const int whole = t[i].rows >> shift, held = whole + (t[i].fresh_base < 0 ? 1 : 0);
+      if (col[i] >= held && col[i] < (t[i].want + mask) >> shift) {
+        int k = (t[i].fresh_base & 0x7fffffff) + col[i] - held;   // its rank among the free pages
+        for (int r = 0; r < (int)(e / W) / b_run; ++r) k += demand_of[r];
         if (k < all_free) {
           int r = 0;
           while (k >= free_of[r]) k -= free_of[r++];
-          page = list[(int64_t)r * p_run + k];
-          a.ref[page] = 1;
-          if (col == whole && (t.rows & mask)) {
-            const int src = checked_page(a.pv, row, col, a.status);
-            if (src >= 0) copies[atomicAdd(n_copies, 1)] = make_int4(src, page, t.rows & mask, 0);
+          page[i] = list[(int64_t)r * p_run + k];
+          a.ref[page[i]] = 1;
+          if (col[i] == whole && (t[i].rows & mask)) {
+            const int src = checked_page(a.pv, a.table + (int64_t)t[i].row * W, col[i], a.status);
+            if (src >= 0) copies[atomicAdd(n_copies, 1)] = make_int4(src, page[i], t[i].rows & mask, 0);
           }
         }
       }
-      out[col] = page;
+      a.table_out[e] = page[i];
     }
   }
   cluster.sync();            // no block leaves while another reads its shared memory
