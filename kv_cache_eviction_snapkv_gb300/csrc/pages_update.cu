@@ -8,10 +8,16 @@
 // lowest first, in the order of (sequence, column). A page that is copied from always keeps
 // a holder, so it is never handed out in the same step.
 //
-// Bound by latency: tables of some 100 KB and one count a page, but four dependent passes over
-// them. So one cluster of eight blocks makes the tables in one launch, with the cluster's
-// hardware barrier between the passes and the blocks' totals in each other's shared memory; a
+// Bound by latency: tables of some 100 KB and two words a page, in dependent passes. A pass
+// over global memory costs some two microseconds before its first result and as much to be seen
+// by the next, so what the passes exchange stays on chip: a cluster of eight blocks (one block
+// where that is enough) holds the pages' counts and lowest users in its shared memory, each
+// block a run of pages, and reaches the others' by remote atomics. What follows from a sequence
+// alone every block works out for itself. That leaves three barriers: state cleared, uses
+// counted, free pages counted; then every free page finds the table entry that it goes to. A
+// pool of more pages than the cluster's shared memory holds keeps the two words in memory. A
 // second, dependent launch copies the started pages' rows with the whole machine.
+#include <algorithm>
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
@@ -23,30 +29,32 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocks = 8;                 // of the cluster
-constexpr int kAtOnce = 8;                 // table entries a thread has in flight
+constexpr int kBlocks = 8;                 // of the cluster, at most
+constexpr int kColumns = 128;              // table columns a warp counts at a time
 constexpr int kTiles = 32;                 // of a page a thread, counted together
 constexpr int kPiece = 16384;              // bytes a block copies at a time
+constexpr int kSharedSeqs = 2048;          // sequences whose records fit shared memory
+constexpr int kSharedPages = 23 * 1024;    // pages whose state fits a block's shared memory
 
-// What new sequence b continues: its parent's table row (-1: none), the rows taken over and the
-// rows it ends up with.
+// What new sequence b continues: its parent's table row (-1: none), the rows taken over, the
+// rows it ends up with, and the rank of its first fresh page (~rank if its started page stays
+// with it).
 struct Taken {
-  int row, rows, want;
-  int fresh_base;            // rank of its first fresh page; the top bit: its started page stays
+  int row, rows, want, base;
 };
 
-// Workspace: Taken [num_out]; copies (source page, target page, rows) [num_out]; owner [num_pages];
-// the blocks' lists of free pages [num_pages]; the number of copies.
+// Workspace: copies (source page, target page, rows) [num_out]; the blocks' records of the
+// sequences [kBlocks][num_out], the first block's always, for the second launch; lowest users
+// [num_pages]; the numbers of copies and of free pages.
 struct Layout {
-  int64_t copies, owner, list, count, bytes;
+  int64_t taken, owner, count, bytes;
 };
 __host__ __device__ inline Layout layout_of(int num_pages, int num_out) {
   Layout l;
-  l.copies = 16 * (int64_t)num_out;
-  l.owner = l.copies + 16 * (int64_t)num_out;
-  l.list = l.owner + 4 * (int64_t)num_pages;
-  l.count = l.list + 4 * (int64_t)num_pages;
-  l.bytes = (l.count + 4 + 15) & ~int64_t(15);
+  l.taken = 16 * (int64_t)num_out;
+  l.owner = l.taken + 16 * (int64_t)num_out * kBlocks;
+  l.count = (l.owner + 4 * (int64_t)num_pages + 7) & ~int64_t(7);
+  l.bytes = (l.count + 8 + 15) & ~int64_t(15);
   return l;
 }
 
@@ -89,167 +97,206 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
   return (warp ? before : 0) + x - v;
 }
 
-__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
-    pages_table_kernel(const __grid_constant__ PagesUpdateArgs a) {
+// blocks: of the cluster, the whole grid. shared_pages: whether the pages' state is in shared
+// memory, p_run pages a block.
+__global__ void __launch_bounds__(kThreads)
+    pages_table_kernel(const __grid_constant__ PagesUpdateArgs a, int blocks, int p_run,
+                       bool shared_pages) {
+  extern __shared__ int smem[];          // counts [p_run], lowest users [p_run]
+  __shared__ Taken shared_take[kSharedSeqs];
   __shared__ int warp_sums[kWarps], tile_sums[kTiles * kWarps];
-  __shared__ int demand_of[kBlocks], free_of[kBlocks];   // every block's, written by their owners
+  __shared__ int free_of[kBlocks];       // every block's, written by their owners
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int gtid = rank * kThreads + tid;
-  constexpr int kAll = kBlocks * kThreads;
+  const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int all = blocks * kThreads, gtid = rank * kThreads + tid;
   const int shift = a.pv.page_shift, mask = a.pv.page_size - 1, P = a.pv.num_pages;
   const Layout lo = layout_of(P, a.num_out);
-  Taken* const take = reinterpret_cast<Taken*>(a.ws);
-  int4* const copies = reinterpret_cast<int4*>(a.ws + lo.copies);
-  int* const owner = reinterpret_cast<int*>(a.ws + lo.owner);
-  int* const list = reinterpret_cast<int*>(a.ws + lo.list);
+  int4* const copies = reinterpret_cast<int4*>(a.ws);
   int* const n_copies = reinterpret_cast<int*>(a.ws + lo.count);
+  Taken* const take = a.num_out <= kSharedSeqs
+                          ? shared_take
+                          : reinterpret_cast<Taken*>(a.ws + lo.taken) + (int64_t)rank * a.num_out;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  auto barrier = [&] {
+    if (blocks == 1) __syncthreads();
+    else cluster.sync();
+  };
 
-  for (int p = gtid; p < P; p += kAll) {
-    a.ref[p] = 0;
-    owner[p] = 0x7fffffff;
+  // the pages' state: any block's, and this block's run
+  const int p0 = (int)min((int64_t)P, (int64_t)rank * p_run), p1 = (int)min((int64_t)P, (int64_t)p0 + p_run);
+  int* const owners = reinterpret_cast<int*>(a.ws + lo.owner);
+  int* const own_count = shared_pages ? smem : a.ref + p0;
+  int* const own_owner = shared_pages ? smem + p_run : owners + p0;
+  auto state_of = [&](int page, int** count, int** owner) {
+    if (shared_pages) {
+      const int r = page / p_run, at = page - r * p_run;
+      int* s = blocks == 1 ? smem : cluster.map_shared_rank(smem, r);
+      *count = s + at;
+      *owner = s + p_run + at;
+    } else {
+      *count = a.ref + page;
+      *owner = owners + page;
+    }
+  };
+  for (int i = tid; i < p1 - p0; i += kThreads) {
+    own_count[i] = 0;
+    own_owner[i] = 0x7fffffff;
   }
-  for (int b = gtid; b < a.num_out; b += kAll) take[b] = taken(a, b);
+  for (int b = tid; b < a.num_out; b += kThreads) take[b] = taken(a, b);
   if (gtid == 0) *n_copies = 0;
-  cluster.sync();
+  barrier();
 
   // whole uses, and the lowest user of every started page
-  const uint32_t W = (uint32_t)a.table_width, entries = (uint32_t)a.num_out * W;
-  for (uint32_t e0 = gtid; e0 < entries; e0 += kAll * kAtOnce) {
-    Taken t[kAtOnce];
+  const int64_t W = a.table_width;
+  const int chunks = (a.table_width + kColumns - 1) / kColumns;
+  const int64_t items = (int64_t)a.num_out * chunks;
+  for (int64_t it = gtid >> 5; it < items; it += all / 32) {
+    const int b = chunks == 1 ? (int)it : (int)(it / chunks);
+    const int c0 = (int)(it - (int64_t)b * chunks) * kColumns;
+    const int row = take[b].row, rows = take[b].rows, whole = rows >> shift;
+    const int last = whole + (rows & mask ? 1 : 0);       // columns in use
+    if (c0 >= last) continue;
+    int page[kColumns / 32];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const uint32_t e = e0 + i * kAll;
-      t[i] = take[e < entries ? e / W : 0];
-      t[i].want = e < entries ? (int)(e % W) : a.table_width;    // the column
+    for (int i = 0; i < kColumns / 32; ++i) {
+      const int col = c0 + lane + 32 * i;
+      page[i] = col < last ? checked_page(a.pv, a.table + row * W, col, a.status) : -1;
     }
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int whole = t[i].rows >> shift, col = t[i].want;
-      if (col > whole || (col == whole && !(t[i].rows & mask))) continue;
-      const int page = checked_page(a.pv, a.table + (int64_t)t[i].row * W, col, a.status);
-      if (page < 0) continue;
-      if (col < whole) atomicAdd(&a.ref[page], 1);
-      else atomicMin(&owner[page], (int)((e0 + i * kAll) / W));
+    for (int i = 0; i < kColumns / 32; ++i) {
+      if (page[i] < 0) continue;
+      int *count, *owner;
+      state_of(page[i], &count, &owner);
+      if (c0 + lane + 32 * i < whole) atomicAdd(count, 1);
+      else atomicMin(owner, b);
     }
   }
-  cluster.sync();
+  barrier();
 
-  // who keeps its started page; the fresh pages' ranks within this block's run of sequences
-  const int b_run = (a.num_out + kBlocks - 1) / kBlocks;
-  const int b0 = min(a.num_out, rank * b_run), b1 = min(a.num_out, b0 + b_run);
-  int demand = 0;
-  for (int bb = b0; bb < b1; bb += kThreads) {
+  // who keeps its started page; the fresh pages' ranks (in every block alike)
+  int wanted = 0;
+  for (int bb = 0; bb < a.num_out; bb += kThreads) {
     const int b = bb + tid;
     int fresh = 0;
-    Taken t;
     bool keeps = false;
-    if (b < b1) {
-      t = take[b];
-      int src = -1;
+    if (b < a.num_out) {
+      const Taken t = take[b];
       if (t.rows & mask) {
-        src = checked_page(a.pv, a.table + (int64_t)t.row * a.table_width, t.rows >> shift, a.status);
-        keeps = src >= 0 && a.ref[src] == 0 && owner[src] == b;   // only its owner changes it here
-        if (keeps) a.ref[src] = 1;
+        const int src = checked_page(a.pv, a.table + t.row * W, t.rows >> shift, a.status);
+        if (src >= 0) {
+          int *count, *owner;
+          state_of(src, &count, &owner);
+          keeps = *count == 0 && *owner == b;
+        }
       }
       fresh = ((t.want + mask) >> shift) - (t.rows >> shift) - (keeps ? 1 : 0);
     }
     int total;
-    const int at = block_prefix(fresh, warp_sums, &total);
-    if (b < b1) take[b].fresh_base = (demand + at) | (keeps ? (int)0x80000000 : 0);
-    demand += total;
+    const int at = wanted + block_prefix(fresh, warp_sums, &total);
+    if (b < a.num_out) take[b].base = keeps ? ~at : at;
+    wanted += total;
   }
-  if (tid < kBlocks) *cluster.map_shared_rank(&demand_of[rank], tid) = demand;
-  cluster.sync();
 
-  // free pages, ascending: a list for every block's run of pages, no longer than the demand
-  int wanted = 0, earlier = 0;
-#pragma unroll
-  for (int r = 0; r < kBlocks; ++r) {
-    wanted += demand_of[r];
-    if (r < rank) earlier += demand_of[r];
+  // A page with a lowest user keeps a holder: that one, or those who hold it whole.
+  auto is_free = [&](int64_t p) { return own_count[p - p0] == 0 && own_owner[p - p0] == 0x7fffffff; };
+  // This block's free pages, ascending: found(page, its number among them) for each.
+  auto each_free = [&](auto found) {
+    int n = 0;
+    for (int64_t pp = p0; pp < p1; pp += kTiles * kThreads) {
+      const int tiles = (int)min((int64_t)kTiles, (p1 - pp + kThreads - 1) / kThreads);
+      uint32_t mine = 0;                 // bit i: page pp + 1024 i + thread is free
+      for (int i = 0; i < tiles; ++i) {
+        const int64_t p = pp + i * kThreads + tid;
+        if (p < p1 && is_free(p)) mine |= 1u << i;
+      }
+      tile_sums[tid] = 0;
+      __syncthreads();
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t m = __ballot_sync(0xffffffffu, mine >> i & 1u);
+        if (lane == 0) tile_sums[i * kWarps + (tid >> 5)] = __popc(m);
+      }
+      __syncthreads();
+      int total;
+      const int before = block_prefix(tile_sums[tid], warp_sums, &total);
+      tile_sums[tid] = n + before;
+      __syncthreads();
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t m = __ballot_sync(0xffffffffu, mine >> i & 1u);
+        if (mine >> i & 1u)
+          found((int)(pp + i * kThreads + tid),
+                tile_sums[i * kWarps + (tid >> 5)] + __popc(m & ((1u << lane) - 1)));
+      }
+      n += total;
+      __syncthreads();
+    }
+  };
+  int nfree;
+  {
+    int n = 0;
+    for (int p = p0 + tid; p < p1; p += kThreads) n += is_free(p);
+    block_prefix(n, warp_sums, &nfree);
   }
-  const int p_run = (P + kBlocks - 1) / kBlocks;
-  const int p0 = (int)min((int64_t)P, (int64_t)rank * p_run), p1 = min(P, p0 + p_run);
-  int nfree = 0;
-  for (int64_t pp = p0; pp < p1; pp += kTiles * kThreads) {
-    const int tiles = (int)min((int64_t)kTiles, (p1 - pp + kThreads - 1) / kThreads);
-    uint32_t mine = 0;                   // bit i: page pp + 1024 i + thread is free
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int64_t p = pp + i * kThreads + tid;
-      if (p < p1 && a.ref[p] == 0) mine |= 1u << i;
-    }
-    tile_sums[tid] = 0;
-    __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
-      const uint32_t all = __ballot_sync(0xffffffffu, mine >> i & 1u);
-      if (lane == 0) tile_sums[i * kWarps + (tid >> 5)] = __popc(all);
-    }
-    __syncthreads();
-    int total;
-    const int before = block_prefix(tile_sums[tid], warp_sums, &total);
-    tile_sums[tid] = nfree + before;
-    __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
-      const uint32_t all = __ballot_sync(0xffffffffu, mine >> i & 1u);
-      const int at = tile_sums[i * kWarps + (tid >> 5)] + __popc(all & ((1u << lane) - 1));
-      if ((mine >> i & 1u) && at < wanted) list[p0 + at] = (int)(pp + i * kThreads + tid);
-    }
-    nfree += total;
-    __syncthreads();
+  if (blocks == 1) {
+    if (tid == 0) free_of[0] = nfree;
+  } else if (tid < blocks) {
+    cluster.map_shared_rank(free_of, tid)[rank] = nfree;
   }
-  if (tid < kBlocks) *cluster.map_shared_rank(&free_of[rank], tid) = nfree;
-  cluster.sync();
+  barrier();
 
-  int all_free = 0;
-#pragma unroll
-  for (int r = 0; r < kBlocks; ++r) all_free += free_of[r];
+  int all_free = 0, before = 0;
+  for (int r = 0; r < blocks; ++r) {
+    if (r < rank) before += free_of[r];
+    all_free += free_of[r];
+  }
   if (gtid == 0) {
+    n_copies[1] = all_free;
     if (a.free_pages) *a.free_pages = all_free - wanted;
     if (wanted > all_free) record_status(a.status, KVSEL_ERR_NO_PAGES);
   }
-  for (uint32_t e0 = gtid; e0 < entries; e0 += kAll * kAtOnce) {
-    Taken t[kAtOnce];
-    int col[kAtOnce], page[kAtOnce];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const uint32_t e = e0 + i * kAll;
-      col[i] = e < entries ? (int)(e % W) : -1;
-      t[i] = take[col[i] < 0 ? 0 : e / W];
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int held = (t[i].rows >> shift) + (t[i].fresh_base < 0 ? 1 : 0);
-      page[i] = -1;
-      if (col[i] >= 0 && col[i] < held)
-        page[i] = checked_page(a.pv, a.table + (int64_t)t[i].row * W, col[i], a.status);
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (col[i] < 0) continue;
-      const uint32_t e = e0 + i * kAll;
-      const int whole = t[i].rows >> shift, held = whole + (t[i].fresh_base < 0 ? 1 : 0);
-      if (col[i] >= held && col[i] < (t[i].want + mask) >> shift) {
-        int k = (t[i].fresh_base & 0x7fffffff) + col[i] - held;   // its rank among the free pages
-        for (int r = 0; r < (int)(e / W) / b_run; ++r) k += demand_of[r];
-        if (k < all_free) {
-          int r = 0;
-          while (k >= free_of[r]) k -= free_of[r++];
-          page[i] = list[(int64_t)r * p_run + k];
-          a.ref[page[i]] = 1;
-          if (col[i] == whole && (t[i].rows & mask)) {
-            const int src = checked_page(a.pv, a.table + (int64_t)t[i].row * W, col[i], a.status);
-            if (src >= 0) copies[atomicAdd(n_copies, 1)] = make_int4(src, page[i], t[i].rows & mask, 0);
-          }
-        }
-      }
-      a.table_out[e] = page[i];
-    }
+  // references: of held pages now, of the free ones as they are handed out
+  for (int i = tid; i < p1 - p0; i += kThreads) {
+    const int n = own_count[i];
+    a.ref[p0 + i] = n ? n : own_owner[i] == 0x7fffffff ? 0 : 1;
   }
-  cluster.sync();            // no block leaves while another reads its shared memory
+  __syncthreads();
+  if (before < wanted) {
+    each_free([&](int page, int k) {
+      k += before;
+      if (k >= wanted) return;
+      auto base_of = [&](int b) { return take[b].base < 0 ? ~take[b].base : take[b].base; };
+      const int b = upper_find(a.num_out, k, base_of);
+      const Taken t = take[b];
+      const int whole = t.rows >> shift, col = whole + (t.base < 0 ? 1 : 0) + k - base_of(b);
+      a.table_out[b * W + col] = page;
+      a.ref[page] = 1;
+      if (col == whole && (t.rows & mask)) {
+        const int src = checked_page(a.pv, a.table + t.row * W, col, a.status);
+        if (src >= 0) copies[atomicAdd(n_copies, 1)] = make_int4(src, page, t.rows & mask, 0);
+      }
+    });
+  }
+  if (rank == 0 && take == shared_take)
+    for (int b = tid; b < a.num_out; b += kThreads)
+      reinterpret_cast<Taken*>(a.ws + lo.taken)[b] = take[b];
+}
+
+// The table entries that are held, and the empty ones (the fresh ones are there).
+__device__ __forceinline__ void other_entries(const PagesUpdateArgs& a, const Layout& lo, int all_free) {
+  const int shift = a.pv.page_shift, mask = a.pv.page_size - 1;
+  const Taken* take = reinterpret_cast<const Taken*>(a.ws + lo.taken);
+  const int64_t W = a.table_width;
+  const uint32_t entries = (uint32_t)(a.num_out * W);        // < 2^31
+  for (uint32_t e = blockIdx.x * blockDim.x + threadIdx.x; e < entries; e += gridDim.x * blockDim.x) {
+    const int b = (int)(e / (uint32_t)W), col = (int)(e - b * (uint32_t)W);
+    const Taken t = take[b];
+    const int held = (t.rows >> shift) + (t.base < 0 ? 1 : 0);
+    int page = -1;
+    if (col < held)
+      page = checked_page(a.pv, a.table + t.row * W, col, a.status);
+    else if (col < (t.want + mask) >> shift && (t.base < 0 ? ~t.base : t.base) + col - held < all_free)
+      continue;
+    a.table_out[e] = page;
+  }
 }
 
 // Rows of started pages for their new holders, in pieces of kPiece bytes: (copy, layer, K or V,
@@ -257,7 +304,9 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__ PagesUpdateArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Layout lo = layout_of(a.pv.num_pages, a.num_out);
-  const int n = *reinterpret_cast<const int*>(a.ws + lo.count);
+  const int2 counts = *reinterpret_cast<const int2*>(a.ws + lo.count);
+  const int n = counts.x;
+  other_entries(a, lo, counts.y);
   const int64_t row_bytes = (int64_t)a.pv.row_units * kRowUnit;
   const int pieces = (int)((row_bytes * (a.pv.page_size - 1) + kPiece - 1) / kPiece);
   const int64_t items = (int64_t)n * a.pv.layers * 2 * pieces;
@@ -266,7 +315,7 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__
     const int64_t from = (it - rest * pieces) * kPiece;
     const int64_t cl = rest >> 1;
     const int layer = (int)(cl % a.pv.layers);
-    const int4 c = reinterpret_cast<const int4*>(a.ws + lo.copies)[cl / a.pv.layers];
+    const int4 c = reinterpret_cast<const int4*>(a.ws)[cl / a.pv.layers];
     const int64_t bytes = min((int64_t)kPiece, c.z * row_bytes - from);
     char* base = (rest & 1 ? a.pv.v : a.pv.k) + layer * a.pv.layer_bytes + from;
     const char* src = base + (int64_t)row_units(a.pv, c.x, 0) * kRowUnit;
@@ -290,15 +339,40 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__
 int64_t pages_update_ws(int num_pages, int num_out) { return layout_of(num_pages, num_out).bytes; }
 
 cudaError_t launch_pages_update(const PagesUpdateArgs& a) {
-  pages_table_kernel<<<kBlocks, kThreads, 0, a.stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  // pages of one row are never started
-  if (e || a.num_out == 0 || a.pv.num_pages == 0 || a.pv.page_size == 1) return e;
+  // One block where it has few pages and columns to count: its barriers are much cheaper. A pool
+  // that the blocks' shared memory does not hold takes eight and global memory.
+  const int64_t items = (int64_t)a.num_out * ((a.table_width + kColumns - 1) / kColumns);
+  const bool one = a.pv.num_pages <= kSharedPages / 4 && items <= 8 * kWarps;
+  const int blocks = one ? 1 : kBlocks;
+  const int p_run = a.pv.num_pages < blocks ? 1 : (int)(((int64_t)a.pv.num_pages + blocks - 1) / blocks);
+  const bool shared_pages = p_run <= kSharedPages;
+  static_assert(kSharedPages * 8 + kSharedSeqs * 16 + 8 * 1024 <= 227 * 1024, "fits shared memory");
+  // always the same value: another thread's call may come between
+  cudaError_t e = cudaFuncSetAttribute(pages_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSharedPages * 8);
+  if (e) return e;
+  {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = shared_pages ? (size_t)p_run * 8 : 0;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, pages_table_kernel, a, blocks, p_run, shared_pages))) return e;
+  }
+  if (a.num_out == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  // as many blocks as there can be pieces, or as the SMs hold at a time
+  // as many blocks as there can be pieces or entries for, or as the SMs hold at a time (pages of
+  // one row are never started)
   const int64_t pieces = ((int64_t)a.pv.row_units * kRowUnit * (a.pv.page_size - 1) + kPiece - 1) / kPiece;
-  const int64_t most = (int64_t)a.num_out * a.pv.layers * 2 * pieces;
-  cfg.gridDim = dim3((unsigned)(most < 8 * (int64_t)a.sm_count ? most : 8 * (int64_t)a.sm_count));
+  const int64_t most = std::max((int64_t)a.num_out * a.pv.layers * 2 * pieces,
+                                ((int64_t)a.num_out * a.table_width + 255) / 256);
+  cfg.gridDim = dim3((unsigned)std::min(most, 8 * (int64_t)a.sm_count));
   cfg.blockDim = dim3(256);
   cfg.stream = a.stream;
   cudaLaunchAttribute at[1];

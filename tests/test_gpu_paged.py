@@ -471,6 +471,18 @@ def test_update_many_sequences_and_pages():
     check_update(c, parents, new)
 
 
+def test_update_more_sequences_and_pages_than_shared_memory_holds():
+    """3000 sequences in a pool of 260000 one-row pages, and 300 columns a table."""
+    rng = np.random.default_rng(6)
+    lens = [int(x) for x in rng.integers(0, 60, size=2999)] + [299]
+    c = Cache(lens, 1, 1, 1, 64, BF16, seed=3, spare=260000 - sum(lens))
+    assert c.P == 260000
+    parents = [int(x) for x in rng.integers(-1, 3000, size=3000)]
+    check_update(c, parents, [min(300, lens[p] + 2) if p >= 0 else 1 for p in parents])
+    c = Cache(lens, 2, 1, 1, 64, BF16, seed=4, spare=5000)
+    check_update(c, parents, [min(300, lens[p] + 1) if p >= 0 else 3 for p in parents])
+
+
 def test_update_shortfall_and_bad_arguments():
     a = api()
     c = Cache([20, 40], 16, 1, 1, 64, BF16, seed=4, spare=1)
