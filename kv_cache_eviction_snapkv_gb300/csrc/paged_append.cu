@@ -13,7 +13,9 @@
 // a head (D * size / 16 lanes a head), in the half layout one from either half, interleaved two
 // neighbours. An element then costs a product and a sum, and no exchange between lanes but the
 // norm's sum. (With 16 contiguous bytes a lane and the other half fetched by shuffles, 16384
-// tokens took 105 us, 74% of the issue slots used.)
+// tokens took 105 us, 74% of the issue slots used.) The loads go through a ring of shared memory,
+// seven heads' rows ahead without a register (four rows ahead in registers: 80 us): every lane
+// copies what it will read itself, so nothing but its own copies is waited for.
 #include "paged.cuh"
 
 namespace kvsel {
@@ -85,14 +87,27 @@ __device__ __forceinline__ int64_t target_row(const AppendArgs& a, int n) {
   return page < 0 ? -1 : (int64_t)row_units(a.pv, page, pos & (a.pv.page_size - 1)) * kRowUnit;
 }
 
+__device__ __forceinline__ void copy8(uint32_t dst, const char* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
 // A warp takes `per_warp` passes of one (layer, token); a pass is 32 / kLanes heads of one
 // kind: all of q's passes, then k's, then v's.
 template <typename T, int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ AppendArgs a,
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a,
                                                              int per_warp) {
   constexpr int U = 8 / sizeof(T), E = 2 * U;     // elements of a unit, of a lane
   constexpr int D = kLanes * E, kHeads = 32 / kLanes, kRowBytes = kLanes * 16;
-  constexpr int kAhead = 4;                       // passes whose loads go out together
+  constexpr int kRing = 8;                        // passes in the ring
+  __shared__ __align__(16) unsigned char ring[kRing][kThreads * 16];
   const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
   const int hk = a.src[1] ? a.pv.Hkv : 0;
   const int pq = (a.H + kHeads - 1) / kHeads, pk = (hk + kHeads - 1) / kHeads;
@@ -111,6 +126,27 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
   const int ua = (apart ? sub : 2 * sub) * 8;     // byte offsets
   const int ub = apart ? ua + half * (int)sizeof(T) : ua + 8;
 
+  const char* from[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    from[i] = a.src[i] + layer * a.layer_bytes[i] + n * a.token_bytes[i] + grp * kRowBytes;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&ring[0][threadIdx.x * 16]);
+  auto issue = [&](int p) {
+    if (p < p1) {
+      const int kind = p < pq ? 0 : p < pq + pk ? 1 : 2;
+      const int h0 = (p - (kind == 0 ? 0 : kind == 1 ? pq : pq + pk)) * kHeads;
+      if (h0 + grp < (kind == 0 ? a.H : hk)) {
+        const char* src = (kind == 0 ? from[0] : kind == 1 ? from[1] : from[2]) + h0 * kRowBytes;
+        const uint32_t to = mine + ((p - p0) & (kRing - 1)) * (kThreads * 16);
+        copy8(to, src + ua);
+        copy8(to + 8, src + ub);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(p0 + i);
+
   const int64_t row = p1 > pq ? target_row(a, n) : -1;
   float c[U], s[U];                               // of this lane's pairs
   const bool rotates = turns && p0 < pq + pk;
@@ -121,15 +157,16 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
       rotation(position, a.inv_freq[sub * U + i], a.rope_scale, &c[i], &s[i]);
   }
 
+  int p = p0;
+#pragma unroll 1
   for (int kind = 0; kind < 3; ++kind) {
     const int first = kind == 0 ? 0 : kind == 1 ? pq : pq + pk;
-    const int b0 = max(p0, first) - first, b1 = min(p1, kind == 0 ? pq : first + pk) - first;
-    if (b0 >= b1) continue;
+    const int end = min(p1, kind == 0 ? pq : first + pk);
+    if (p >= end) continue;
     const int heads = kind == 0 ? a.H : hk;
-    if (kind > 0 && row < 0) continue;
-    const char* src = a.src[kind] + layer * a.layer_bytes[kind] + n * a.token_bytes[kind];
     char* dst = kind == 0 ? a.q_out + ((int64_t)layer * a.tokens + n) * a.H * kRowBytes
                           : (kind == 1 ? a.pv.k : a.pv.v) + layer * a.pv.layer_bytes + row;
+    const bool placed = kind == 0 || row >= 0;
     const char* weight = kind == 0 ? a.weight[0] : kind == 1 ? a.weight[1] : nullptr;
     // the pair (x, y) becomes (x ca - y sb, y cb + x sa) g: cosines and sines times weights
     float ca[U], sa[U], cb[U], sb[U];
@@ -151,56 +188,47 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
         sb[i] = rotates ? wy * s[i] : 0.f;
       }
     }
-    for (int p = b0; p < b1; p += kAhead) {
-      uint2 va[kAhead], vb[kAhead];
+#pragma unroll 2
+    for (; p < end; ++p) {
+      issue(p + kRing - 1);                       // into the slot that was read a pass ago
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      const uint4 v = shared16(mine + ((p - p0) & (kRing - 1)) * (kThreads * 16));
+      const int h = (p - first) * kHeads + grp;
+      uint2 ya = make_uint2(v.x, v.y), yb = make_uint2(v.z, v.w);
+      if (kind < 2) {
+        float x[E], r[E];
+        unpack<T>(ya, x);
+        unpack<T>(yb, x + U);
+        float g = 1.f;
+        if (weight) {
+          float ss = 0.f;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int h = (p + u) * kHeads + grp;
-        va[u] = vb[u] = make_uint2(0, 0);
-        if (p + u < b1 && h < heads) {
-          va[u] = __ldcs(reinterpret_cast<const uint2*>(src + h * kRowBytes + ua));
-          vb[u] = __ldcs(reinterpret_cast<const uint2*>(src + h * kRowBytes + ub));
+          for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+          for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          g = rsqrtf(ss * (1.f / D) + a.eps);
         }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int ix = kInterleaved ? 2 * i : i, iy = kInterleaved ? 2 * i + 1 : U + i;
+          r[ix] = x[ix] * ca[i];
+          r[iy] = x[iy] * cb[i];
+          if (turns) {                 // elsewhere an infinite neighbour must stay out
+            r[ix] = fmaf(-x[iy], sb[i], r[ix]);
+            r[iy] = fmaf(x[ix], sa[i], r[iy]);
+          }
+        }
+        if (weight) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) r[i] *= g;
+        }
+        ya = pack<T>(r);
+        yb = pack<T>(r + U);
       }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (p + u >= b1) break;
-        const int h = (p + u) * kHeads + grp;
-        uint2 ya = va[u], yb = vb[u];
-        if (kind < 2) {
-          float x[E], r[E];
-          unpack<T>(va[u], x);
-          unpack<T>(vb[u], x + U);
-          float g = 1.f;
-          if (weight) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            g = rsqrtf(ss * (1.f / D) + a.eps);
-          }
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-            const int ix = kInterleaved ? 2 * i : i, iy = kInterleaved ? 2 * i + 1 : U + i;
-            r[ix] = x[ix] * ca[i];
-            r[iy] = x[iy] * cb[i];
-            if (turns) {               // elsewhere an infinite neighbour must stay out
-              r[ix] = fmaf(-x[iy], sb[i], r[ix]);
-              r[iy] = fmaf(x[ix], sa[i], r[iy]);
-            }
-          }
-          if (weight) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) r[i] *= g;
-          }
-          ya = pack<T>(r);
-          yb = pack<T>(r + U);
-        }
-        if (h < heads) {
-          *reinterpret_cast<uint2*>(dst + (int64_t)h * kRowBytes + ua) = ya;
-          *reinterpret_cast<uint2*>(dst + (int64_t)h * kRowBytes + ub) = yb;
-        }
+      if (placed && h < heads) {
+        char* to = dst + (int64_t)h * kRowBytes;
+        *reinterpret_cast<uint2*>(to + ua) = ya;
+        *reinterpret_cast<uint2*>(to + ub) = yb;
       }
     }
   }

@@ -31,7 +31,9 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 8;                 // of the cluster, at most
 constexpr int kColumns = 128;              // table columns a warp counts at a time
-constexpr int kTiles = 32;                 // of a page a thread, counted together
+constexpr int kItems = 4;                  // such pieces that it has in flight
+constexpr int kTiles = 8;                  // of a page a thread, numbered together
+static_assert(kTiles * kWarps <= kThreads, "a thread a count");
 constexpr int kPiece = 16384;              // bytes a block copies at a time
 constexpr int kSharedSeqs = 2048;          // sequences whose records fit shared memory
 constexpr int kSharedPages = 23 * 1024;    // pages whose state fits a block's shared memory
@@ -150,31 +152,42 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t W = a.table_width;
   const int chunks = (a.table_width + kColumns - 1) / kColumns;
   const int64_t items = (int64_t)a.num_out * chunks;
-  for (int64_t it = gtid >> 5; it < items; it += all / 32) {
-    const int b = chunks == 1 ? (int)it : (int)(it / chunks);
-    const int c0 = (int)(it - (int64_t)b * chunks) * kColumns;
-    const int row = take[b].row, rows = take[b].rows, whole = rows >> shift;
-    const int last = whole + (rows & mask ? 1 : 0);       // columns in use
-    if (c0 >= last) continue;
-    int page[kColumns / 32];
+  constexpr int kCols = kColumns / 32;
+  for (int64_t it0 = gtid >> 5; it0 < items; it0 += all / 32 * kItems) {
+    int page[kItems][kCols], b[kItems], c0[kItems], whole[kItems];
 #pragma unroll
-    for (int i = 0; i < kColumns / 32; ++i) {
-      const int col = c0 + lane + 32 * i;
-      page[i] = col < last ? checked_page(a.pv, a.table + row * W, col, a.status) : -1;
+    for (int j = 0; j < kItems; ++j) {
+      const int64_t it = it0 + j * (all / 32);
+      const bool in = it < items;
+      b[j] = !in ? 0 : chunks == 1 ? (int)it : (int)(it / chunks);
+      c0[j] = in ? (int)(it - (int64_t)b[j] * chunks) * kColumns + lane : 0;
+      const Taken t = take[b[j]];
+      whole[j] = t.rows >> shift;
+      const int last = in ? whole[j] + (t.rows & mask ? 1 : 0) : 0;      // columns in use
+#pragma unroll
+      for (int i = 0; i < kCols; ++i)
+        page[j][i] = c0[j] + 32 * i < last ? max(__ldg(a.table + t.row * W + c0[j] + 32 * i), -1) : -2;
     }
 #pragma unroll
-    for (int i = 0; i < kColumns / 32; ++i) {
-      if (page[i] < 0) continue;
-      int *count, *owner;
-      state_of(page[i], &count, &owner);
-      if (c0 + lane + 32 * i < whole) atomicAdd(count, 1);
-      else atomicMin(owner, b);
-    }
+    for (int j = 0; j < kItems; ++j)
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        if (page[j][i] == -2) continue;
+        if (page[j][i] < 0 || page[j][i] >= P) {
+          record_status(a.status, KVSEL_ERR_BAD_INDEX);
+          continue;
+        }
+        int *count, *owner;
+        state_of(page[j][i], &count, &owner);
+        if (c0[j] + 32 * i < whole[j]) atomicAdd(count, 1);
+        else atomicMin(owner, b[j]);
+      }
   }
   barrier();
 
   // who keeps its started page; the fresh pages' ranks (in every block alike)
   int wanted = 0;
+#pragma unroll 1
   for (int bb = 0; bb < a.num_out; bb += kThreads) {
     const int b = bb + tid;
     int fresh = 0;
@@ -199,17 +212,17 @@ __global__ void __launch_bounds__(kThreads)
 
   // A page with a lowest user keeps a holder: that one, or those who hold it whole.
   auto is_free = [&](int64_t p) { return own_count[p - p0] == 0 && own_owner[p - p0] == 0x7fffffff; };
-  // This block's free pages, ascending: found(page, its number among them) for each.
-  auto each_free = [&](auto found) {
+  // This block's first `most` free pages or more, ascending: found(page, its number) for each.
+  auto each_free = [&](int most, auto found) {
     int n = 0;
-    for (int64_t pp = p0; pp < p1; pp += kTiles * kThreads) {
+    for (int64_t pp = p0; pp < p1 && n < most; pp += kTiles * kThreads) {
       const int tiles = (int)min((int64_t)kTiles, (p1 - pp + kThreads - 1) / kThreads);
       uint32_t mine = 0;                 // bit i: page pp + 1024 i + thread is free
       for (int i = 0; i < tiles; ++i) {
         const int64_t p = pp + i * kThreads + tid;
         if (p < p1 && is_free(p)) mine |= 1u << i;
       }
-      tile_sums[tid] = 0;
+      if (tid < kTiles * kWarps) tile_sums[tid] = 0;
       __syncthreads();
       for (int i = 0; i < tiles; ++i) {
         const uint32_t m = __ballot_sync(0xffffffffu, mine >> i & 1u);
@@ -217,8 +230,8 @@ __global__ void __launch_bounds__(kThreads)
       }
       __syncthreads();
       int total;
-      const int before = block_prefix(tile_sums[tid], warp_sums, &total);
-      tile_sums[tid] = n + before;
+      const int at = n + block_prefix(tid < kTiles * kWarps ? tile_sums[tid] : 0, warp_sums, &total);
+      if (tid < kTiles * kWarps) tile_sums[tid] = at;
       __syncthreads();
       for (int i = 0; i < tiles; ++i) {
         const uint32_t m = __ballot_sync(0xffffffffu, mine >> i & 1u);
@@ -230,10 +243,22 @@ __global__ void __launch_bounds__(kThreads)
       __syncthreads();
     }
   };
+  // Free pages of this block's run, and the held pages' references (the free ones get theirs as
+  // they are handed out). In memory the counts are the references already, but for the started
+  // pages', which other blocks may still be reading.
   int nfree;
   {
     int n = 0;
-    for (int p = p0 + tid; p < p1; p += kThreads) n += is_free(p);
+    if (shared_pages) {
+      for (int i = tid; i < p1 - p0; i += kThreads) {
+        const int c = own_count[i];
+        const bool started = own_owner[i] != 0x7fffffff;
+        n += c == 0 && !started;
+        a.ref[p0 + i] = c ? c : started;
+      }
+    } else {
+      for (int p = p0 + tid; p < p1; p += kThreads) n += is_free(p);
+    }
     block_prefix(n, warp_sums, &nfree);
   }
   if (blocks == 1) {
@@ -253,14 +278,12 @@ __global__ void __launch_bounds__(kThreads)
     if (a.free_pages) *a.free_pages = all_free - wanted;
     if (wanted > all_free) record_status(a.status, KVSEL_ERR_NO_PAGES);
   }
-  // references: of held pages now, of the free ones as they are handed out
-  for (int i = tid; i < p1 - p0; i += kThreads) {
-    const int n = own_count[i];
-    a.ref[p0 + i] = n ? n : own_owner[i] == 0x7fffffff ? 0 : 1;
-  }
+  if (!shared_pages)
+    for (int i = tid; i < p1 - p0; i += kThreads)
+      if (own_count[i] == 0 && own_owner[i] != 0x7fffffff) own_count[i] = 1;
   __syncthreads();
   if (before < wanted) {
-    each_free([&](int page, int k) {
+    each_free(wanted - before, [&](int page, int k) {
       k += before;
       if (k >= wanted) return;
       auto base_of = [&](int b) { return take[b].base < 0 ? ~take[b].base : take[b].base; };
