@@ -11,17 +11,17 @@
 // instructions, so a warp keeps one token's cosines and sines, times the norm's weights, for as
 // many of its heads as leave the machine full, and a lane holds whole pairs: two 8-byte units of
 // a head (D * size / 16 lanes a head), in the half layout one from either half, interleaved two
-// neighbours. An element then costs a product and a sum, and no exchange between lanes but the
-// norm's sum. (With 16 contiguous bytes a lane and the other half fetched by shuffles, 16384
-// tokens took 105 us, 74% of the issue slots used.) The loads go through a ring of shared memory,
-// seven heads' rows ahead without a register (four rows ahead in registers: 80 us): every lane
-// copies what it will read itself, so nothing but its own copies is waited for.
+// neighbours. An element then costs a product and a sum, two elements at a time (the fp32 pair
+// instructions), and no exchange between lanes but the norm's sum. (With 16 contiguous bytes a
+// lane and the other half fetched by shuffles, 16384 tokens took 105 us, 74% of the issue slots
+// used.) The loads go through a ring of shared memory, seven passes ahead without a register:
+// every lane copies what it will read itself, so nothing but its own copies is waited for.
 #include "paged.cuh"
 
 namespace kvsel {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;   // small blocks: the last ones leave less of the machine idle
 
 // cos and sin of position * f, times scale. The angle in turns, position * f / (2 pi), is a
 // sum of exact products: f / (2 pi) as two floats, the position as two parts of 16 bits, and
@@ -45,27 +45,58 @@ __device__ __forceinline__ void rotation(int position, float f, float scale, flo
   *s *= scale;
 }
 
-// An 8-byte unit: four bf16 or two fp32 values.
+// Two fp32 values and the instructions on them.
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// 16 bytes of a row: eight bf16 or four fp32 values, in twos.
 template <typename T>
-__device__ __forceinline__ void unpack(const uint2& v, float* x) {
-  if constexpr (sizeof(T) == 2) {
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
-  } else {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
+__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[8 / sizeof(T)]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
+    if constexpr (sizeof(T) == 2)
+      x[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else
+      x[i] = two(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
   }
 }
 template <typename T>
-__device__ __forceinline__ uint2 pack(const float* x) {
-  if constexpr (sizeof(T) == 2) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    return make_uint2(__float_as_uint(x[0]), __float_as_uint(x[1]));
+__device__ __forceinline__ uint4 pack(const Two (&x)[8 / sizeof(T)]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
+    const float2 f = both(x[i]);
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      w[2 * i] = __float_as_uint(f.x);
+      w[2 * i + 1] = __float_as_uint(f.y);
+    }
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Where token n's key and value rows go within a layer, in bytes; -1: nowhere.
@@ -102,12 +133,13 @@ __device__ __forceinline__ uint4 shared16(uint32_t a) {
 // A warp takes `per_warp` passes of one (layer, token); a pass is 32 / kLanes heads of one
 // kind: all of q's passes, then k's, then v's.
 template <typename T, int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a,
+__global__ void __launch_bounds__(kThreads, 7) append_kernel(const __grid_constant__ AppendArgs a,
                                                              int per_warp) {
-  constexpr int U = 8 / sizeof(T), E = 2 * U;     // elements of a unit, of a lane
-  constexpr int D = kLanes * E, kHeads = 32 / kLanes, kRowBytes = kLanes * 16;
+  constexpr int N = 8 / sizeof(T), U = N;         // twos of a lane, its pairs
+  constexpr int D = kLanes * 2 * N, kHeads = 32 / kLanes, kRowBytes = kLanes * 16;
   constexpr int kRing = 8;                        // passes in the ring
-  __shared__ __align__(16) unsigned char ring[kRing][kThreads * 16];
+  constexpr int kSlot = kThreads * 16;
+  __shared__ __align__(16) unsigned char ring[kRing][kSlot];
   const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
   const int hk = a.src[1] ? a.pv.Hkv : 0;
   const int pq = (a.H + kHeads - 1) / kHeads, pk = (hk + kHeads - 1) / kHeads;
@@ -120,34 +152,46 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
 
   // this lane's units of a head: (i, i + rot/2) for the lanes that turn in the half layout, two
   // neighbours else
-  const int half = a.rot / 2, turning = a.rot / E;
-  const bool turns = sub < turning;
+  const bool turns = sub < a.rot / (2 * N);
   const bool apart = !kInterleaved && turns;
   const int ua = (apart ? sub : 2 * sub) * 8;     // byte offsets
-  const int ub = apart ? ua + half * (int)sizeof(T) : ua + 8;
+  const int ub = apart ? ua + a.rot / 2 * (int)sizeof(T) : ua + 8;
 
-  const char* from[3];
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    from[i] = a.src[i] + layer * a.layer_bytes[i] + n * a.token_bytes[i] + grp * kRowBytes;
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&ring[0][threadIdx.x * 16]);
-  auto issue = [&](int p) {
-    if (p < p1) {
-      const int kind = p < pq ? 0 : p < pq + pk ? 1 : 2;
-      const int h0 = (p - (kind == 0 ? 0 : kind == 1 ? pq : pq + pk)) * kHeads;
-      if (h0 + grp < (kind == 0 ? a.H : hk)) {
-        const char* src = (kind == 0 ? from[0] : kind == 1 ? from[1] : from[2]) + h0 * kRowBytes;
-        const uint32_t to = mine + ((p - p0) & (kRing - 1)) * (kThreads * 16);
-        copy8(to, src + ua);
-        copy8(to + 8, src + ub);
-      }
+  // the heads of passes [b, e) of a kind that this lane's group has, and the first one's place
+  auto heads_of = [&](int b, int e, int heads) {
+    const int h = (heads - b * kHeads - grp + kHeads - 1) / kHeads;
+    return max(0, min(e - b, h));
+  };
+  const char* src = nullptr;
+  int left = 0;
+  uint32_t in = mine;
+  auto issue = [&] {
+    if (left > 0) {
+      copy8(in, src + ua);
+      copy8(in + 8, src + ub);
     }
+    src += kHeads * kRowBytes;
+    --left;
+    in = in == mine + (kRing - 1) * kSlot ? mine : in + kSlot;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  auto begin = [&](int kind, int b, int e) {
+    src = a.src[kind] + layer * a.layer_bytes[kind] + n * a.token_bytes[kind] +
+          (b * kHeads + grp) * kRowBytes;
+    left = heads_of(b, e, kind == 0 ? a.H : hk);
+    in = mine;
 #pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) issue(p0 + i);
+    for (int i = 0; i < kRing - 1; ++i) issue();
+  };
 
+  const int q0 = min(p0, pq), q1 = min(p1, pq);
+  const int k0 = min(max(p0 - pq, 0), pk), k1 = min(max(p1 - pq, 0), pk);
+  const int v0 = min(max(p0 - pq - pk, 0), pk), v1 = min(max(p1 - pq - pk, 0), pk);
+  if (q0 < q1) begin(0, q0, q1);
+  else if (k0 < k1) begin(1, k0, k1);
   const int64_t row = p1 > pq ? target_row(a, n) : -1;
+
   float c[U], s[U];                               // of this lane's pairs
   const bool rotates = turns && p0 < pq + pk;
   if (rotates) {
@@ -156,80 +200,98 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
     for (int i = 0; i < U; ++i)
       rotation(position, a.inv_freq[sub * U + i], a.rope_scale, &c[i], &s[i]);
   }
-
-  int p = p0;
 #pragma unroll 1
-  for (int kind = 0; kind < 3; ++kind) {
-    const int first = kind == 0 ? 0 : kind == 1 ? pq : pq + pk;
-    const int end = min(p1, kind == 0 ? pq : first + pk);
-    if (p >= end) continue;
-    const int heads = kind == 0 ? a.H : hk;
+  for (int kind = 0; kind < 2; ++kind) {
+    const int b = kind == 0 ? q0 : k0, e = kind == 0 ? q1 : k1;
+    if (b >= e) continue;
+    if (kind == 1 && q0 < q1) begin(1, k0, k1);
     char* dst = kind == 0 ? a.q_out + ((int64_t)layer * a.tokens + n) * a.H * kRowBytes
-                          : (kind == 1 ? a.pv.k : a.pv.v) + layer * a.pv.layer_bytes + row;
-    const bool placed = kind == 0 || row >= 0;
-    const char* weight = kind == 0 ? a.weight[0] : kind == 1 ? a.weight[1] : nullptr;
-    // the pair (x, y) becomes (x ca - y sb, y cb + x sa) g: cosines and sines times weights
-    float ca[U], sa[U], cb[U], sb[U];
-    if (kind < 2) {
-      float w[E];
+                          : a.pv.k + layer * a.pv.layer_bytes + row;
+    dst += (int64_t)(b * kHeads + grp) * kRowBytes;
+    int out = kind == 0 || row >= 0 ? heads_of(b, e, kind == 0 ? a.H : hk) : 0;
+    const char* weight = kind == 0 ? a.weight[0] : a.weight[1];
+    // twos v, with w the other elements of their pairs, become (v va + w vb) g: cosines and
+    // sines times weights
+    Two va[N], vb[N];
+    {
+      Two w[N];
 #pragma unroll
-      for (int i = 0; i < E; ++i) w[i] = 1.f;
+      for (int i = 0; i < N; ++i) w[i] = two(1.f, 1.f);
       if (weight) {
         const char* at = weight + (int64_t)layer * kRowBytes;
-        unpack<T>(*reinterpret_cast<const uint2*>(at + ua), w);
-        unpack<T>(*reinterpret_cast<const uint2*>(at + ub), w + U);
+        const uint2 x = *reinterpret_cast<const uint2*>(at + ua), y = *reinterpret_cast<const uint2*>(at + ub);
+        unpack<T>(make_uint4(x.x, x.y, y.x, y.y), w);
       }
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const float wx = kInterleaved ? w[2 * i] : w[i], wy = kInterleaved ? w[2 * i + 1] : w[U + i];
-        ca[i] = rotates ? wx * c[i] : wx;
-        sa[i] = rotates ? wx * s[i] : 0.f;
-        cb[i] = rotates ? wy * c[i] : wy;
-        sb[i] = rotates ? wy * s[i] : 0.f;
+      for (int i = 0; i < N; ++i) {
+        va[i] = w[i];
+        vb[i] = two(0.f, 0.f);
+        if (!rotates) continue;
+        if (kInterleaved) {
+          const float2 f = both(w[i]);
+          va[i] = mul(w[i], two(c[i], c[i]));
+          vb[i] = two(-f.y * s[i], f.x * s[i]);
+        } else {
+          const int j = 2 * (i % (N / 2));
+          const float sign = i < N / 2 ? -1.f : 1.f;
+          va[i] = mul(w[i], two(c[j], c[j + 1]));
+          vb[i] = mul(w[i ^ (N / 2)], two(sign * s[j], sign * s[j + 1]));
+        }
       }
     }
+    uint32_t at = mine;
 #pragma unroll 2
-    for (; p < end; ++p) {
-      issue(p + kRing - 1);                       // into the slot that was read a pass ago
+    for (int p = b; p < e; ++p) {
+      issue();                                    // into the slot that was read a pass ago
       asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-      const uint4 v = shared16(mine + ((p - p0) & (kRing - 1)) * (kThreads * 16));
-      const int h = (p - first) * kHeads + grp;
-      uint2 ya = make_uint2(v.x, v.y), yb = make_uint2(v.z, v.w);
-      if (kind < 2) {
-        float x[E], r[E];
-        unpack<T>(ya, x);
-        unpack<T>(yb, x + U);
-        float g = 1.f;
-        if (weight) {
-          float ss = 0.f;
+      const uint4 raw = shared16(at);
+      at = at == mine + (kRing - 1) * kSlot ? mine : at + kSlot;
+      Two x[N], r[N];
+      unpack<T>(raw, x);
 #pragma unroll
-          for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-          for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-          g = rsqrtf(ss * (1.f / D) + a.eps);
+      for (int i = 0; i < N; ++i) {
+        r[i] = mul(x[i], va[i]);
+        if (turns) {                              // elsewhere an infinite neighbour must stay out
+          const float2 f = both(x[i]);
+          r[i] = fma(kInterleaved ? two(f.y, f.x) : x[i ^ (N / 2)], vb[i], r[i]);
         }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int ix = kInterleaved ? 2 * i : i, iy = kInterleaved ? 2 * i + 1 : U + i;
-          r[ix] = x[ix] * ca[i];
-          r[iy] = x[iy] * cb[i];
-          if (turns) {                 // elsewhere an infinite neighbour must stay out
-            r[ix] = fmaf(-x[iy], sb[i], r[ix]);
-            r[iy] = fmaf(x[ix], sa[i], r[iy]);
-          }
-        }
-        if (weight) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) r[i] *= g;
-        }
-        ya = pack<T>(r);
-        yb = pack<T>(r + U);
       }
-      if (placed && h < heads) {
-        char* to = dst + (int64_t)h * kRowBytes;
-        *reinterpret_cast<uint2*>(to + ua) = ya;
-        *reinterpret_cast<uint2*>(to + ub) = yb;
+      if (weight) {
+        Two ss = mul(x[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < N; ++i) ss = fma(x[i], x[i], ss);
+        const float2 f = both(ss);
+        float sum = f.x + f.y;
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const float g = rsqrtf(fmaf(sum, 1.f / D, a.eps));
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = mul(r[i], two(g, g));
       }
+      const uint4 y = pack<T>(r);
+      if (out > 0) {
+        *reinterpret_cast<uint2*>(dst + ua) = make_uint2(y.x, y.y);
+        *reinterpret_cast<uint2*>(dst + ub) = make_uint2(y.z, y.w);
+      }
+      dst += kHeads * kRowBytes;
+      --out;
+    }
+  }
+  // v, as it is
+  if (v0 < v1 && row >= 0) {
+    const int64_t first = (int64_t)(v0 * kHeads + grp) * kRowBytes + sub * 16;
+    const char* from = a.src[2] + layer * a.layer_bytes[2] + n * a.token_bytes[2] + first;
+    char* to = a.pv.v + layer * a.pv.layer_bytes + row + first;
+    const int heads = heads_of(v0, v1, hk);
+    for (int i0 = 0; i0 < heads; i0 += 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < heads)
+          v[i] = __ldcs(reinterpret_cast<const uint4*>(from + (i0 + i) * (kHeads * kRowBytes)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < heads) *reinterpret_cast<uint4*>(to + (i0 + i) * (kHeads * kRowBytes)) = v[i];
     }
   }
 }
