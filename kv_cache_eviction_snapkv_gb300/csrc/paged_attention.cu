@@ -98,10 +98,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(b), "f"(a));
   return y;
 }
-// x = hi + lo in two tf32 values: 22 bits of x.
+// x = hi + lo in two tf32 values, 21 bits or more of x: hi rounded, so that what is cut off of lo
+// has no common sign (it would shift every logit), in plain instructions where the conversions
+// take several. NaN and infinities leave a NaN in lo.
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(*hi) : "f"(__uint_as_float(x)));
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(*lo) : "f"(__uint_as_float(x) - __uint_as_float(*hi)));
+  *hi = (x + 0x1000u) & 0xffffe000u;
+  *lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(*hi)) & 0xffffe000u;
 }
 
 // A warp's step: 16 rows x 8 * NT heads. Lane (g, t) = (lane / 4, lane % 4) holds of S^T rows g
@@ -193,7 +195,8 @@ struct Step {
   // S^T of this step's rows and heads.
   __device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t stage, int lane) const {
     const int g = lane >> 2, t = lane & 3;
-    float acc[NT][2][4] = {};
+    constexpr int kAcc = kEb == 2 ? 2 : 4;       // short chains of dependent products
+    float acc[NT][kAcc][4] = {};
     const uint32_t row = stage + g * kRowBytes;
 #pragma unroll
     for (int c = 0; c < kKw / 4; ++c) {
@@ -212,9 +215,9 @@ struct Step {
 #pragma unroll
             for (int i = 0; i < 4; ++i) split_tf32(e[k][i], &h[i], &w[i]);
             const uint32_t* f = &qf[x][8 * c + 4 * k];
-            mma_tf32(acc[x][0], h[0], h[1], h[2], h[3], f[0], f[1]);
-            mma_tf32(acc[x][1], w[0], w[1], w[2], w[3], f[0], f[1]);
-            mma_tf32(acc[x][1], h[0], h[1], h[2], h[3], f[2], f[3]);
+            mma_tf32(acc[x][k], h[0], h[1], h[2], h[3], f[0], f[1]);
+            mma_tf32(acc[x][2], w[0], w[1], w[2], w[3], f[0], f[1]);
+            mma_tf32(acc[x][3], h[0], h[1], h[2], h[3], f[2], f[3]);
           }
         }
       }
@@ -222,15 +225,17 @@ struct Step {
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[x][i] = acc[x][0][i] + acc[x][1][i];
+      for (int i = 0; i < 4; ++i) {
+        s[x][i] = acc[x][0][i] + acc[x][1][i];
+        if constexpr (kAcc == 4) s[x][i] += acc[x][2][i] + acc[x][3][i];
+      }
   }
 
-  // Running maximum and sum; s becomes the weights.
-  __device__ __forceinline__ void weigh(float (&s)[NT][4], uint32_t valid, float scale, int lane) {
+  // Running maximum and sum; s becomes the weights, f the factors of what was there before.
+  __device__ __forceinline__ void weigh(float (&s)[NT][4], float (&f)[NT][2], uint32_t valid,
+                                        float scale, int lane) {
     const int g = lane >> 2;
     const bool ok0 = valid >> g & 1u, ok1 = valid >> (g + 8) & 1u;
-    bool moved = false;
-    float f[NT][2];
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -244,35 +249,28 @@ struct Step {
         mx = fmaxf(mx, m[x][c]);
         const float ref = mx == -INFINITY ? 0.f : mx;
         f[x][c] = ex2(m[x][c] - ref);
-        moved |= mx != m[x][c];
         m[x][c] = mx;
         // -inf gives 0; NaN (and +inf, whose maximum it is) gives NaN
         s[x][c] = ex2(s[x][c] - ref);
         s[x][2 + c] = ex2(s[x][2 + c] - ref);
+        l[x][c] = fmaf(l[x][c], f[x][c], s[x][c] + s[x][2 + c]);
       }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        l[x][0] *= f[x][0];
-        l[x][1] *= f[x][1];
-#pragma unroll
-        for (int i = 0; i < kMt; ++i) {
-          o[x][i][0] *= f[x][0];
-          o[x][i][1] *= f[x][1];
-          o[x][i][2] *= f[x][0];
-          o[x][i][3] *= f[x][1];
-        }
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      l[x][0] += s[x][0] + s[x][2];
-      l[x][1] += s[x][1] + s[x][3];
-    }
   }
 
-  // O^T += V^T P^T; p: this lane's weights, in S^T's places.
-  __device__ __forceinline__ void values(const float (&p)[NT][4], uint32_t stage, int lane) {
+  // O^T = O^T f + V^T P^T; p: this lane's weights, in S^T's places. The product of a step is
+  // formed from zero and added in fp32: the matrix unit cuts off what it adds to, and over the
+  // thousands of steps of a long cache that cost 2e-5 of the result.
+  __device__ __forceinline__ void add(float (&to)[4], const float (&f)[2], const float (&d)[4]) {
+    const Two ff = two(f[0], f[1]);
+    const float2 a = both(fma(two(to[0], to[1]), ff, two(d[0], d[1])));
+    const float2 b = both(fma(two(to[2], to[3]), ff, two(d[2], d[3])));
+    to[0] = a.x;
+    to[1] = a.y;
+    to[2] = b.x;
+    to[3] = b.y;
+  }
+  __device__ __forceinline__ void values(const float (&p)[NT][4], const float (&f)[NT][2], uint32_t stage,
+                                         int lane) {
     const int g = lane >> 2, t = lane & 3;
     uint32_t bh[NT][kEb], bl[NT][kEb];
 #pragma unroll
@@ -313,13 +311,16 @@ struct Step {
           const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
 #pragma unroll
           for (int x = 0; x < NT; ++x) {
-            mma_bf16(o[x][c * 4 + i], a0, a1, a2, a3, bh[x][0], bh[x][1]);
-            mma_bf16(o[x][c * 4 + i], a0, a1, a2, a3, bl[x][0], bl[x][1]);
+            float d[4] = {};
+            mma_bf16(d, a0, a1, a2, a3, bh[x][0], bh[x][1]);
+            mma_bf16(d, a0, a1, a2, a3, bl[x][0], bl[x][1]);
+            add(o[x][c * 4 + i], f[x], d);
           }
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          float d[NT][4] = {};
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             uint32_t h[4], w[4];
@@ -329,12 +330,14 @@ struct Step {
             split_tf32(v[2 * k + 1][2 * i + 1], &h[3], &w[3]);
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-              float (&d)[4] = o[x][c * 2 + i];
-              mma_tf32(d, h[0], h[1], h[2], h[3], bh[x][2 * k], bh[x][2 * k + 1]);
-              mma_tf32(d, w[0], w[1], w[2], w[3], bh[x][2 * k], bh[x][2 * k + 1]);
-              mma_tf32(d, h[0], h[1], h[2], h[3], bl[x][2 * k], bl[x][2 * k + 1]);
+              mma_tf32(d[x], h[0], h[1], h[2], h[3], bh[x][2 * k], bh[x][2 * k + 1]);
+              mma_tf32(d[x], w[0], w[1], w[2], w[3], bh[x][2 * k], bh[x][2 * k + 1]);
+              mma_tf32(d[x], h[0], h[1], h[2], h[3], bl[x][2 * k], bl[x][2 * k + 1]);
             }
           }
+#pragma unroll
+          for (int x = 0; x < NT; ++x) add(o[x][c * 2 + i], f[x], d[x]);
+        }
       }
     }
   }
@@ -505,10 +508,10 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
       copy_step(slot == 0 ? St::kStages - 1 : slot - 1);
       const uint32_t stage = ring + slot * St::kStage, v = valid[slot];
       if (v) {
-        float s[NT][4];
+        float s[NT][4], f[NT][2];
         st.scores(s, stage, lane);
-        st.weigh(s, v, a.scale_log2, lane);
-        st.values(s, stage, lane);
+        st.weigh(s, f, v, a.scale_log2, lane);
+        st.values(s, f, stage, lane);
       }
       slot = slot == St::kStages - 1 ? 0 : slot + 1;
     }
