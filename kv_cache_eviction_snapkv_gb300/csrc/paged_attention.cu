@@ -195,7 +195,7 @@ struct Step {
   // S^T of this step's rows and heads.
   __device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t stage, int lane) const {
     const int g = lane >> 2, t = lane & 3;
-    constexpr int kAcc = kEb == 2 ? 2 : 4;       // short chains of dependent products
+    constexpr int kAcc = 4;                      // short chains: the matrix unit cuts off at every link
     float acc[NT][kAcc][4] = {};
     const uint32_t row = stage + g * kRowBytes;
 #pragma unroll
@@ -205,8 +205,8 @@ struct Step {
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
         if constexpr (kEb == 2) {
-          mma_bf16(acc[x][0], a.x, b.x, a.y, b.y, qf[x][4 * c], qf[x][4 * c + 1]);
-          mma_bf16(acc[x][1], a.z, b.z, a.w, b.w, qf[x][4 * c + 2], qf[x][4 * c + 3]);
+          mma_bf16(acc[x][(2 * c) % kAcc], a.x, b.x, a.y, b.y, qf[x][4 * c], qf[x][4 * c + 1]);
+          mma_bf16(acc[x][(2 * c + 1) % kAcc], a.z, b.z, a.w, b.w, qf[x][4 * c + 2], qf[x][4 * c + 3]);
         } else {
           const uint32_t e[2][4] = {{a.x, b.x, a.y, b.y}, {a.z, b.z, a.w, b.w}};
 #pragma unroll
@@ -226,8 +226,11 @@ struct Step {
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[x][i] = acc[x][0][i] + acc[x][1][i];
-        if constexpr (kAcc == 4) s[x][i] += acc[x][2][i] + acc[x][3][i];
+#pragma unroll
+        for (int w = kAcc / 2; w > 0; w /= 2)
+#pragma unroll
+          for (int k = 0; k < w; ++k) acc[x][k][i] += acc[x][k + w][i];
+        s[x][i] = acc[x][0][i];
       }
   }
 
@@ -272,19 +275,23 @@ struct Step {
   __device__ __forceinline__ void values(const float (&p)[NT][4], const float (&f)[NT][2], uint32_t stage,
                                          int lane) {
     const int g = lane >> 2, t = lane & 3;
-    uint32_t bh[NT][kEb], bl[NT][kEb];
+    uint32_t bh[NT][kEb], bl[NT][kEb], br[NT][2];
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float p0 = p[x][2 * i], p1 = p[x][2 * i + 1];
         if constexpr (kEb == 2) {
-          // weights as a sum of two bf16 (2^-17 of the weight): one would cost 2^-9
+          // weights as a sum of three bf16, 24 bits: with two the results were off by 1e-6, with
+          // one by 1e-3, and the time is the same
           const uint32_t hi = pack_bf16(p0, p1);
-          const uint32_t lo = pack_bf16(p0 - __uint_as_float(hi << 16),
-                                        p1 - __uint_as_float(hi & 0xffff0000u));
+          const float p2 = p0 - __uint_as_float(hi << 16), p3 = p1 - __uint_as_float(hi & 0xffff0000u);
+          const uint32_t lo = pack_bf16(p2, p3);
+          const uint32_t rest = pack_bf16(p2 - __uint_as_float(lo << 16),
+                                          p3 - __uint_as_float(lo & 0xffff0000u));
           bh[x][i] = transposed(hi);
           bl[x][i] = transposed(lo);
+          br[x][i] = transposed(rest);
         } else {
           // transposed in two halves; then rows 2t, 2t + 1 (+ 8) of head g
           const uint32_t u = __float_as_uint(p0), w = __float_as_uint(p1);
@@ -312,8 +319,9 @@ struct Step {
 #pragma unroll
           for (int x = 0; x < NT; ++x) {
             float d[4] = {};
-            mma_bf16(d, a0, a1, a2, a3, bh[x][0], bh[x][1]);
+            mma_bf16(d, a0, a1, a2, a3, br[x][0], br[x][1]);
             mma_bf16(d, a0, a1, a2, a3, bl[x][0], bl[x][1]);
+            mma_bf16(d, a0, a1, a2, a3, bh[x][0], bh[x][1]);
             add(o[x][c * 4 + i], f[x], d);
           }
         }

@@ -57,8 +57,8 @@ __device__ __forceinline__ int batch_prefix(const bool (&flag)[kBatch], int (&be
   return __shfl_sync(0xffffffffu, x, 31);
 }
 
-// Blocks (layer, sequence, head) x parts. Shared: the bitmap of kept rows < n, the movers'
-// list entries and the holes' slots (16 bits each: max_keep <= 32768).
+// Blocks (layer, sequence, head) x parts. Shared: the movers' rows, the bitmap of kept rows < n
+// and the holes' slots (16 bits: max_keep <= 32768).
 __global__ void __launch_bounds__(kThreads, 4) paged_compact_kernel(const __grid_constant__ PagedCompactArgs a,
                                                                     int parts) {
   extern __shared__ uint32_t smem[];
@@ -79,51 +79,53 @@ __global__ void __launch_bounds__(kThreads, 4) paged_compact_kernel(const __grid
     return;
   }
   const int words = (n + 31) >> 5;
-  uint32_t* kept = smem;
-  uint16_t* mover = reinterpret_cast<uint16_t*>(smem + ((a.max_keep + 31) >> 5));
-  uint16_t* hole = mover + ((a.max_keep + 1) & ~1);
+  int* mover = reinterpret_cast<int*>(smem);
+  uint32_t* kept = smem + a.max_keep;
+  uint16_t* hole = reinterpret_cast<uint16_t*>(kept + ((a.max_keep + 31) >> 5));
   const int32_t* trow = a.table + (int64_t)b * a.table_width;
   for (int w = tid; w < words; w += kThreads) kept[w] = 0;
   if (tid == 0) bad = 0;
   __syncthreads();
-  if (n < len) {
-    for (int col = tid; col < (n + a.pv.page_size - 1) >> a.pv.page_shift; col += kThreads) {
-      const int page = checked_page(a.pv, trow, col, a.status);
-      if (page < 0) {
-        bad = 1;
-      } else if (a.ref && a.ref[page] > 1) {
-        record_status(a.status, KVSEL_ERR_SHARED_PAGE);
-        bad = 1;
-      }
-    }
-  }
   const int32_t* list = a.keep_idx + ((int64_t)layer * a.keep_rows + o0) * a.pv.Hkv + h;
   int movers = 0;
   for (int s0 = 0; s0 < n; s0 += kThreads * kBatch) {
-    int idx[kBatch], at[kBatch];
+    int idx[kBatch], page[kBatch], at[kBatch];
     bool late[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int s = s0 + i * kThreads + tid;
       idx[i] = s < n ? list[(int64_t)s * a.pv.Hkv] : 0;
     }
+    if (s0 == 0 && n < len) {            // while the list arrives: the pages that may be written
+      for (int col = tid; col < (n + a.pv.page_size - 1) >> a.pv.page_shift; col += kThreads) {
+        const int p = checked_page(a.pv, trow, col, a.status);
+        if (p < 0) {
+          bad = 1;
+        } else if (a.ref && a.ref[p] > 1) {
+          record_status(a.status, KVSEL_ERR_SHARED_PAGE);
+          bad = 1;
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int s = s0 + i * kThreads + tid;
-      late[i] = s < n && idx[i] >= n;
-      if (s >= n) continue;
-      if (idx[i] < 0 || idx[i] >= len) {
+      late[i] = s0 + i * kThreads + tid < n && idx[i] >= n;
+      page[i] = late[i] && idx[i] < len ? __ldg(trow + (idx[i] >> a.pv.page_shift)) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (s0 + i * kThreads + tid >= n) continue;
+      // out of range, on a page out of range, or named twice
+      if (idx[i] < 0 || idx[i] >= len || (late[i] && (page[i] < 0 || page[i] >= a.pv.num_pages)) ||
+          (!late[i] && (atomicOr(&kept[idx[i] >> 5], 1u << (idx[i] & 31)) >> (idx[i] & 31) & 1u))) {
         bad = 1;
-        record_status(a.status, KVSEL_ERR_BAD_INDEX);
-      } else if (!late[i] && (atomicOr(&kept[idx[i] >> 5], 1u << (idx[i] & 31)) >> (idx[i] & 31) & 1u)) {
-        bad = 1;                         // named twice
         record_status(a.status, KVSEL_ERR_BAD_INDEX);
       }
     }
     const int total = batch_prefix(late, at, counts);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (late[i]) mover[movers + at[i]] = (uint16_t)(s0 + i * kThreads + tid);
+      if (late[i]) mover[movers + at[i]] = idx[i];
     movers += total;
   }
   __syncthreads();                       // the bitmap is whole
@@ -142,10 +144,6 @@ __global__ void __launch_bounds__(kThreads, 4) paged_compact_kernel(const __grid
       if (gap[i]) hole[holes + at[i]] = (uint16_t)(s0 + i * kThreads + tid);
     holes += total;
   }
-  // a mover's page out of range: every part has to know, so every part looks at all movers
-  for (int i = tid; i < movers; i += kThreads)
-    if (checked_page(a.pv, trow, list[(int64_t)mover[i] * a.pv.Hkv] >> a.pv.page_shift, a.status) < 0)
-      bad = 1;
   __syncthreads();
   if (bad) return;                       // uniform; holes == movers from here on
   int32_t* pos = a.slot_pos ? a.slot_pos + ((int64_t)layer * a.keep_rows + o0) * a.pv.Hkv + h : nullptr;
@@ -161,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_compact_kernel(const __grid
   for (int c0 = m0; c0 < m1; c0 += kChunk) {
     const int c = min(kChunk, m1 - c0);
     for (int i = tid; i < c; i += kThreads) {
-      const int slot = hole[c0 + i], row = list[(int64_t)mover[c0 + i] * a.pv.Hkv];
+      const int slot = hole[c0 + i], row = mover[c0 + i];
       from[i] = row_units(a.pv, trow[row >> a.pv.page_shift], row & (a.pv.page_size - 1));
       to[i] = row_units(a.pv, trow[slot >> a.pv.page_shift], slot & (a.pv.page_size - 1));
       if (pos) pos[(int64_t)slot * a.pv.Hkv] = row;
@@ -196,9 +194,9 @@ __global__ void __launch_bounds__(kThreads, 4) paged_compact_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_paged_compact(const PagedCompactArgs& a) {
-  static_assert((kMaxKeep / 32) * 4 + 4 * kMaxKeep + 2 * kChunk * 4 + 1024 <= 227 * 1024,
+  static_assert((kMaxKeep / 32) * 4 + 6 * kMaxKeep + 2 * kChunk * 4 + 1024 <= 227 * 1024,
                 "lists and offsets fit shared memory");
-  auto lists = [](int n) { return ((n + 31) >> 5) * 4 + 2 * ((n + 1) & ~1) * 2; };
+  auto lists = [](int n) { return n * 4 + ((n + 31) >> 5) * 4 + ((n + 1) & ~1) * 2; };
   const int smem = lists(a.max_keep);
   if (smem > 32 * 1024) {
     // always the same value: another thread's call may come between
