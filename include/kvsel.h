@@ -453,7 +453,8 @@ kvsel_status kvsel_paged_append(const kvsel_pages* pages, int32_t num_tokens, in
  * [num_layers][num_seqs][num_heads] fp32 natural log, or NULL. A sequence of
  * length 0 gets out = 0, lse = -inf. Rows behind the length are never read.
  * workspace: kvsel_paged_attention_bytes(pages, num_seqs, num_heads) bytes, 16-byte
- * aligned. Repeated calls on the same inputs give the same bits. Rules:
+ * aligned. Calls with the same arguments give the same bits (other lengths in the
+ * batch may change a sequence's last bits: the work is split by all of them). Rules:
  * INVALID_ARG for num_heads that H_kv does not divide, a workspace that is too
  * small or misaligned; UNSUPPORTED for num_seqs > 8192, num_layers * num_seqs *
  * num_heads >= 2^31 or num_seqs * table_width * page_size > 2^35. Device status: BAD_INDEX for a length outside

@@ -34,7 +34,7 @@ constexpr int kSegment = 2;
 // Units that are worth a part of their own: one sequence of 293 rows took 9.7 us with 4, 8.1
 // with 2.
 constexpr int kLeast = 2;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;  // small, so that a block for every warp of the first launch fits at once
 
 // What the launch fixes; the rest follows from the lengths.
 struct AttnGeom {
@@ -44,14 +44,16 @@ struct AttnGeom {
   int grid;
 };
 
-// Workspace: what each warp's split instance is, then the partials [warps][2][heads]: base-2
-// max and sum, and the weighted values [D].
+// Workspace: the split instances that each warp has a piece of, the partials [warps][2][heads]:
+// base-2 max and sum, and the weighted values [D]. An instance's first piece is in slot 1 of its
+// warp, the others in slot 0.
 struct SplitInfo {
-  int64_t first_head; // index of its first query head in out / D, -1: no instance to join
-  int last;           // last warp that has a piece of it
-  int heads;
+  int64_t first_head; // index of its first query head in out / D, -1: none
+  int first, last;    // the warps that have its pieces
+  int heads, pad;
 };
-__host__ __device__ inline int64_t ws_ml(int warps) { return 16 * (int64_t)warps; }
+constexpr int kInfo = 2 * sizeof(SplitInfo);           // [0]: went on from an earlier warp, [1]: began here
+__host__ __device__ inline int64_t ws_ml(int warps) { return kInfo * (int64_t)warps; }
 __host__ __device__ inline int64_t ws_acc(int warps, int heads) {
   return ws_ml(warps) + ((16 * (int64_t)warps * heads + 15) & ~int64_t(15));
 }
@@ -418,7 +420,14 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
   const int64_t units = per_layer * a.pv.layers;
   const int parts = (int)min((int64_t)warps, (units + kLeast - 1) / kLeast);
   const int part = blockIdx.x * kWarps + warp;
-  auto part_start = [&](int64_t c) { return quotient(c * units, parts); };
+  // the first `longer` parts have a unit more than the others
+  const int64_t each = parts ? quotient(units, parts) : 0;
+  const int longer = (int)(units - each * parts);
+  auto part_start = [&](int64_t c) { return c * each + min(c, (int64_t)longer); };
+  auto part_of = [&](int64_t unit) {
+    const int64_t split = (each + 1) * longer;
+    return (int)(unit < split ? quotient(unit, each + 1) : longer + quotient(unit - split, each));
+  };
   const bool works = part < parts;
   const int64_t u0 = works ? part_start(part) : 0, u1 = works ? part_start(part + 1) : 0;
 
@@ -482,7 +491,9 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
     copies_commit();
   };
 
-  SplitInfo info{-1, 0, 0};
+  // lane 0's own, so that a later one comes after
+  SplitInfo* const info = reinterpret_cast<SplitInfo*>(a.ws) + 2 * part;
+  if (lane == 0) info[0].first_head = info[1].first_head = -1;
   float2* const ml = reinterpret_cast<float2*>(a.ws + ws_ml(warps));
   float* const acc = reinterpret_cast<float*>(a.ws + ws_acc(warps, gm.heads));
 
@@ -528,14 +539,11 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
     const int64_t at = ((int64_t)part * 2 + (begins ? 1 : 0)) * gm.heads;
     const int64_t first = first_head;
     const int heads = n_heads;
-    if (begins && !whole) {
-      // its last piece is the last part's that starts before its end
-      const int64_t end = x.end + (x.n_steps - x.last);
-      info.first_head = first;
-      info.heads = heads;
-      info.last = (int)min((int64_t)parts - 1, quotient(end * parts, units));
-      while (part_start(info.last) >= end) --info.last;
-      while (info.last + 1 < parts && part_start(info.last + 1) < end) ++info.last;
+    if (!whole && lane == 0) {
+      // a piece that goes on starts with step x.first; the instance ends after its last step
+      const int64_t stop = x.end + (x.n_steps - x.last);
+      info[begins ? 1 : 0] = SplitInfo{first, begins ? part : part_of(u - x.first), part_of(stop - 1),
+                                       heads, 0};
     }
     u = x.end;
     next();                            // its queries arrive while this one's results go out
@@ -567,40 +575,50 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
       }
     if (bad) record_status(a.status, KVSEL_ERR_NONFINITE);
   }
-  if (lane == 0) reinterpret_cast<SplitInfo*>(a.ws)[part] = info;
 }
 
-// Joins the pieces of the instance that starts in part c and ends in a later one, if there is
-// one: slot 1 of c, then slot 0 of the parts up to `last`. The block's warps share the heads, and
-// the pieces of a head where there are fewer heads than warps; every warp keeps a maximum of its
-// own, so that one round of loads does.
+// Joins the split instances' pieces. An instance that spans the parts first .. last is joined by
+// the blocks first .. last, its heads shared out among them. A block's warps share its heads (of
+// the instance that goes on in its part and of the one that begins there), and the pieces of a
+// head where there are fewer heads than warps; every warp keeps a maximum of its own, so that one
+// round of loads does where the pieces are few.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a,
+__global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __grid_constant__ PagedAttnArgs a,
                                                                   const __grid_constant__ AttnGeom gm) {
-  constexpr int kJoinWarps = kJoinThreads / 32, E = D / 32, kAhead = 8;
-  __shared__ float maxs[kJoinWarps], sums[kJoinWarps], vals[kJoinWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+  constexpr int kJoinWarps = kJoinThreads / 32, E = D / 32, kAhead = 4;
+  __shared__ float maxs[kJoinWarps], sums[kJoinWarps];
+  __shared__ __align__(16) float vals[kJoinWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = gm.grid * kWarps;
-  int per = kJoinWarps;                       // warps a head: a power of two
-  while (per > 1 && per * gm.heads > kJoinWarps) per >>= 1;
-  const int sub = warp & (per - 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float2* ml = reinterpret_cast<const float2*>(a.ws + ws_ml(warps));
   const float* acc = reinterpret_cast<const float*>(a.ws + ws_acc(warps, gm.heads));
-  const SplitInfo info = reinterpret_cast<const SplitInfo*>(a.ws)[c];
-  if (info.first_head < 0) return;
-  const int n = info.last - c + 1;
-  for (int h0 = 0; h0 < info.heads; h0 += kJoinWarps / per) {
-    const int h = h0 + warp / per;
+  const SplitInfo* infos = reinterpret_cast<const SplitInfo*>(a.ws) + 2 * blockIdx.x;
+  const SplitInfo on = infos[0], begun = infos[1];
+  // heads of either that are this block's: its place among the parts, then every n-th
+  auto share = [&](const SplitInfo& i) {
+    const int n = i.last - i.first + 1, at = blockIdx.x - i.first;
+    return i.first_head < 0 || at >= i.heads ? 0 : (i.heads - at + n - 1) / n;
+  };
+  const int count0 = share(on), count = count0 + share(begun);
+  if (count == 0) return;
+  int per = kJoinWarps;                       // warps a head: a power of two
+  while (per > 1 && per * count > kJoinWarps) per >>= 1;
+  const int sub = warp & (per - 1);
+  for (int c0 = 0; c0 < count; c0 += kJoinWarps / per) {
+    const int c = c0 + warp / per;
+    const SplitInfo& info = c < count0 ? on : begun;
+    const int n = info.last - info.first + 1;
+    const int h = (int)blockIdx.x - info.first + (c < count0 ? c : c - count0) * n;
     float mx = -INFINITY, sum = 0.f, v[E] = {};
-    if (h < info.heads) {
+    if (c < count) {
       for (int i0 = sub; i0 < n; i0 += per * kAhead) {
         float2 y[kAhead];
         float w[kAhead][E];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           const int i = i0 + k * per;
-          const int64_t at = ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * gm.heads + h;
+          const int64_t at = ((int64_t)(info.first + i) * 2 + (i == 0 ? 1 : 0)) * gm.heads + h;
           y[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int e = 0; e < E; ++e) w[k][e] = 0.f;
@@ -637,29 +655,28 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 #pragma unroll
     for (int e = 0; e < E; ++e) vals[warp][lane * E + e] = v[e];
     __syncthreads();
-    if (sub == 0 && h < info.heads) {
-      float top = mx;
-      for (int w = 1; w < per; ++w) top = fmaxf(top, maxs[warp + w]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float total = 0.f, r[E] = {};
-      for (int w = 0; w < per; ++w) {
-        const float f = ex2(maxs[warp + w] - ref);
-        total = fmaf(sums[warp + w], f, total);
+    if (sub != 0 || c >= count) continue;
+    float top = mx;
+    for (int w = 1; w < per; ++w) top = fmaxf(top, maxs[warp + w]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float total = 0.f, r[E] = {};
+    for (int w = 0; w < per; ++w) {
+      const float f = ex2(maxs[warp + w] - ref);
+      total = fmaf(sums[warp + w], f, total);
 #pragma unroll
-        for (int e = 0; e < E; ++e) r[e] = fmaf(vals[warp + w][lane * E + e], f, r[e]);
-      }
-      bool bad = !finite_f(total);
-      float* out = a.out + (info.first_head + h) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        r[e] = total == 0.f ? 0.f : r[e] / total;
-        bad |= !finite_f(r[e]);
-        out[e] = r[e];
-      }
-      if (lane == 0 && a.lse)
-        a.lse[info.first_head + h] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
-      if (bad) record_status(a.status, KVSEL_ERR_NONFINITE);
+      for (int e = 0; e < E; ++e) r[e] = fmaf(vals[warp + w][lane * E + e], f, r[e]);
     }
+    bool bad = !finite_f(total);
+    float* out = a.out + (info.first_head + h) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      r[e] = total == 0.f ? 0.f : r[e] / total;
+      bad |= !finite_f(r[e]);
+      out[e] = r[e];
+    }
+    if (lane == 0 && a.lse)
+      a.lse[info.first_head + h] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
+    if (bad) record_status(a.status, KVSEL_ERR_NONFINITE);
   }
 }
 

@@ -163,7 +163,10 @@ def test_attention_bad_lengths_pages_and_values():
         np.testing.assert_allclose(f64(out)[0, 0, h], ref, rtol=1e-4, atol=2e-5)
     out, lse = a.kvsel_paged_attention(q, c.K, c.V, c.table, ints([-5, 20]))
     assert status() == a.KVSEL_ERR_BAD_INDEX
-    assert not out[:, 0].any() and torch.equal(out[:, 1], good[:, 1])
+    # other lengths cut the rows into other runs, so sequence 1's sums differ by their rounding:
+    # the bound for any order of 32-bit sums holds, equal bits are promised for equal arguments only
+    o, _, ob, _ = pg.attention(f64(q), f64(c.K), f64(c.V), c.table.cpu().numpy(), [0, 20])
+    assert not out[:, 0].any() and (np.abs(f64(out) - o) <= ob).all()
     a.kvsel_paged_attention(q, c.K, c.V, c.table, ints([40, 1 << 30]))   # held to the table's rows
     assert status() == a.KVSEL_ERR_BAD_INDEX
     c.K[0, c.table[1, 0], 3] = float("inf")
