@@ -434,7 +434,8 @@ kvsel_status kvsel_rope_frequencies(int32_t rot_dim, double base, int32_t kind, 
  * Two tokens must not name the same row. Rules: INVALID_ARG for negative
  * counts, eps < 0 or not finite, misaligned rows, seqs NULL with num_tokens >
  * num_seqs, k without v; UNSUPPORTED for a rot_dim that is no multiple of 16 or
- * above D, and for num_heads + 2 * H_kv > 65535. Device status: BAD_INDEX
+ * above D, for num_heads + 2 * H_kv > 65535, and for num_layers * num_tokens *
+ * (num_heads + 2 * H_kv) >= 2^32. Device status: BAD_INDEX
  * for a sequence, row or page out of range (that token's k and v are not
  * written). Asynchronous; capturable. */
 kvsel_status kvsel_paged_append(const kvsel_pages* pages, int32_t num_tokens, int32_t num_heads,
@@ -457,9 +458,10 @@ kvsel_status kvsel_paged_append(const kvsel_pages* pages, int32_t num_tokens, in
  * batch may change a sequence's last bits: the work is split by all of them). Rules:
  * INVALID_ARG for num_heads that H_kv does not divide, a workspace that is too
  * small or misaligned; UNSUPPORTED for num_seqs > 8192, num_layers * num_seqs *
- * num_heads >= 2^31 or num_seqs * table_width * page_size > 2^35. Device status: BAD_INDEX for a length outside
- * [0, table_width * page_size] (taken as the nearer end) or a page out of range
- * (its rows are left out), NONFINITE if a sum or an output is not finite.
+ * num_heads >= 2^31 or num_seqs * table_width * page_size > 2^34. Device status:
+ * BAD_INDEX for a length outside [0, table_width * page_size] (taken as the
+ * nearer end) or a page out of range (its rows are left out), NONFINITE if a sum
+ * or an output is not finite (fp32: also for values of 2^127 or more).
  * Asynchronous; capturable. */
 kvsel_status kvsel_paged_attention(const kvsel_pages* pages, int32_t num_seqs, int32_t num_heads,
                                    const void* q, const int32_t* table, int32_t table_width,
@@ -483,7 +485,7 @@ int64_t kvsel_paged_attention_bytes(const kvsel_pages* pages, int32_t num_seqs,
  * [num_layers][keep_rows][H_kv] int32 (or NULL; not keep_idx's own memory): the row that each
  * slot now holds.
  * keep_offsets [num_seqs + 1] int32 on the device, nondecreasing from 0.
- * max_keep: an upper bound on n. ref [num_pages] int32 (or NULL: not checked): the
+ * max_keep: an upper bound on n (0: nothing is done). ref [num_pages] int32 (or NULL: not checked): the
  * references from kvsel_pages_update; a sequence whose slots 0 .. n-1 touch a page with
  * ref > 1 while n < lens[b] is left whole and SHARED_PAGE recorded.
  * Rules: INVALID_ARG for num_seqs < 0, max_keep < 0, keep_rows < 0; UNSUPPORTED for

@@ -28,6 +28,11 @@ __device__ __forceinline__ int checked_len(int len, int max_rows, int* status) {
   return len < 0 ? 0 : max_rows;
 }
 
+// x / y, x >= 0, y > 0: mostly small, and a division of 32 bits is several times cheaper.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+}
+
 // Two fp32 values and the instructions on them.
 struct Two {
   uint64_t v;

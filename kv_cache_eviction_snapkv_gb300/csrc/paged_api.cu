@@ -114,7 +114,9 @@ kvsel_status kvsel_paged_append(const kvsel_pages* pages, int32_t num_tokens, in
   const int rot = rope ? rope->rot_dim : 0;
   if (rot < 0 || (rot > 0 && !std::isfinite(rope->scale))) return KVSEL_ERR_INVALID_ARG;
   if (rot > a.pv.D || rot % 16) return KVSEL_ERR_UNSUPPORTED;
-  if ((int64_t)num_heads + 2 * (int64_t)a.pv.Hkv > 65535) return KVSEL_ERR_UNSUPPORTED;
+  const int64_t heads = (int64_t)num_heads + 2 * (int64_t)a.pv.Hkv;
+  if (heads > 65535 || (double)a.pv.layers * num_tokens * (double)heads >= 4294967296.0)
+    return KVSEL_ERR_UNSUPPORTED;
   if (k && table) {
     if ((st = check_table(a.pv, num_seqs, table, table_width))) return st;
     if (!seqs && num_tokens > num_seqs) return KVSEL_ERR_INVALID_ARG;
@@ -190,7 +192,7 @@ kvsel_status kvsel_paged_attention(const kvsel_pages* pages, int32_t num_seqs, i
   if ((st = attention_view(pages, true, num_seqs, num_heads, &a.pv))) return st;
   if ((st = check_table(a.pv, num_seqs, table, table_width))) return st;
   if (num_seqs == 0) return KVSEL_OK;
-  if ((int64_t)num_seqs * table_width > (int64_t(1) << 35) / a.pv.page_size)
+  if ((int64_t)num_seqs * table_width > (int64_t(1) << 34) / a.pv.page_size)
     return KVSEL_ERR_UNSUPPORTED;
   if (!q || !lens || !out || misaligned(q, kRowUnit) || misaligned(out, 16))
     return KVSEL_ERR_INVALID_ARG;

@@ -283,7 +283,6 @@ cudaError_t launch(const AppendArgs& a) {
   per = per < 1 ? 1 : per > passes ? passes : per;
   const int64_t warps = rows * ((passes + per - 1) / per);
   const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (a.interleaved)
     append_kernel<T, kLanes, true><<<(unsigned)blocks, kThreads, 0, a.stream>>>(a, (int)per);
   else

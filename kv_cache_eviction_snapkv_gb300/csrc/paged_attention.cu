@@ -353,10 +353,6 @@ struct Step {
   }
 };
 
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-  return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
-}
-
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ AttnGeom gm) {

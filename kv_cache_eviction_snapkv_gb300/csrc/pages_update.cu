@@ -34,7 +34,7 @@ constexpr int kColumns = 128;              // table columns a warp counts at a t
 constexpr int kItems = 4;                  // such pieces that it has in flight
 constexpr int kTiles = 8;                  // of a page a thread, numbered together
 static_assert(kTiles * kWarps <= kThreads, "a thread a count");
-constexpr int kPiece = 16384;              // bytes a block copies at a time
+constexpr int kPiece = 32768;              // bytes a block copies at a time
 constexpr int kSharedSeqs = 2048;          // sequences whose records fit shared memory
 constexpr int kSharedPages = 23 * 1024;    // pages whose state fits a block's shared memory
 
@@ -100,10 +100,10 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
 }
 
 // blocks: of the cluster, the whole grid. shared_pages: whether the pages' state is in shared
-// memory, p_run pages a block.
+// memory, p_run pages a block; run_inverse = ceil(2^40 / p_run) for these.
 __global__ void __launch_bounds__(kThreads)
     pages_table_kernel(const __grid_constant__ PagesUpdateArgs a, int blocks, int p_run,
-                       bool shared_pages) {
+                       uint32_t run_inverse, bool shared_pages) {
   extern __shared__ int smem[];          // counts [p_run], lowest users [p_run]
   __shared__ Taken shared_take[kSharedSeqs];
   __shared__ int warp_sums[kWarps], tile_sums[kTiles * kWarps];
@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(kThreads)
   int* const own_owner = shared_pages ? smem + p_run : owners + p0;
   auto state_of = [&](int page, int** count, int** owner) {
     if (shared_pages) {
-      const int r = page / p_run, at = page - r * p_run;
+      // page / p_run: exact, as page * p_run < 2^40
+      const int r = blocks == 1 ? 0 : (int)((uint64_t)page * run_inverse >> 40), at = page - r * p_run;
       int* s = blocks == 1 ? smem : cluster.map_shared_rank(smem, r);
       *count = s + at;
       *owner = s + p_run + at;
@@ -333,26 +334,39 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__
   const int64_t row_bytes = (int64_t)a.pv.row_units * kRowUnit;
   const int pieces = (int)((row_bytes * (a.pv.page_size - 1) + kPiece - 1) / kPiece);
   const int64_t items = (int64_t)n * a.pv.layers * 2 * pieces;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t rest = it / pieces;
+  struct Piece {
+    char* src;
+    char* dst;
+    int bytes;
+  };
+  auto piece = [&](int64_t it) {
+    Piece x{nullptr, nullptr, 0};
+    if (it >= items) return x;
+    const int64_t rest = quotient(it, pieces);
     const int64_t from = (it - rest * pieces) * kPiece;
-    const int64_t cl = rest >> 1;
-    const int layer = (int)(cl % a.pv.layers);
-    const int4 c = reinterpret_cast<const int4*>(a.ws)[cl / a.pv.layers];
-    const int64_t bytes = min((int64_t)kPiece, c.z * row_bytes - from);
+    const int64_t cl = rest >> 1, at = quotient(cl, a.pv.layers);
+    const int layer = (int)(cl - at * a.pv.layers);
+    const int4 c = reinterpret_cast<const int4*>(a.ws)[at];
     char* base = (rest & 1 ? a.pv.v : a.pv.k) + layer * a.pv.layer_bytes + from;
-    const char* src = base + (int64_t)row_units(a.pv, c.x, 0) * kRowUnit;
-    char* dst = base + (int64_t)row_units(a.pv, c.y, 0) * kRowUnit;
+    x.src = base + (int64_t)row_units(a.pv, c.x, 0) * kRowUnit;
+    x.dst = base + (int64_t)row_units(a.pv, c.y, 0) * kRowUnit;
+    x.bytes = (int)max((int64_t)0, min((int64_t)kPiece, c.z * row_bytes - from));
+    return x;
+  };
+  Piece next = piece(blockIdx.x);
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const Piece x = next;
     uint4 v[kPiece / 4096];
 #pragma unroll
     for (int i = 0; i < kPiece / 4096; ++i) {
       const int e = (i * 256 + threadIdx.x) * 16;
-      if (e < bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + e));
+      if (e < x.bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(x.src + e));
     }
+    next = piece(it + gridDim.x);          // while this one's rows arrive
 #pragma unroll
     for (int i = 0; i < kPiece / 4096; ++i) {
       const int e = (i * 256 + threadIdx.x) * 16;
-      if (e < bytes) *reinterpret_cast<uint4*>(dst + e) = v[i];
+      if (e < x.bytes) *reinterpret_cast<uint4*>(x.dst + e) = v[i];
     }
   }
 }
@@ -368,8 +382,9 @@ cudaError_t launch_pages_update(const PagesUpdateArgs& a) {
   const int64_t items = (int64_t)a.num_out * ((a.table_width + kColumns - 1) / kColumns);
   const bool one = a.pv.num_pages <= kSharedPages / 4 && items <= 4 * kWarps;
   const int blocks = one ? 1 : kBlocks;
-  const int p_run = a.pv.num_pages < blocks ? 1 : (int)(((int64_t)a.pv.num_pages + blocks - 1) / blocks);
+  const int p_run = (int)std::max<int64_t>(((int64_t)a.pv.num_pages + blocks - 1) / blocks, 1024);
   const bool shared_pages = p_run <= kSharedPages;
+  const uint32_t run_inverse = (uint32_t)(((uint64_t(1) << 40) + p_run - 1) / p_run);
   static_assert(kSharedPages * 8 + kSharedSeqs * 16 + 8 * 1024 <= 227 * 1024, "fits shared memory");
   // always the same value: another thread's call may come between
   cudaError_t e = cudaFuncSetAttribute(pages_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -387,7 +402,8 @@ cudaError_t launch_pages_update(const PagesUpdateArgs& a) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, pages_table_kernel, a, blocks, p_run, shared_pages))) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, pages_table_kernel, a, blocks, p_run, run_inverse, shared_pages)))
+      return e;
   }
   if (a.num_out == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg{};

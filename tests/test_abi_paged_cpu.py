@@ -88,6 +88,7 @@ def test_null_pool(lib):
     (dict(H=3), 1), (dict(H=0), 1), (dict(S=-1), 1), (dict(q=None), 1), (dict(q=ODD), 1),
     (dict(table=None), 1), (dict(width=0), 1), (dict(lens=None), 1), (dict(out=None), 1),
     (dict(out=ODD), 1), (dict(width=1 << 27), 2), (dict(S=8193), 2),
+    (dict(S=8192, width=(1 << 17) + 1), 2),
 ])
 def test_attention_rules(lib, kw, status):
     assert attention(lib, pool(), **kw) == status
@@ -101,7 +102,7 @@ def test_append_rules(lib):
                        (dict(w=ODD), 1), (dict(q=rows(4096 + 8)), 1), (dict(k=rows(token=12)), 1),
                        (dict(v=rows(layer=-8)), 1), (dict(q=rows(None)), 1), (dict(rope=16, pos=None), 1),
                        (dict(rope=-16), 1), (dict(rope=20), 2), (dict(rope=144), 2), (dict(H=65532), 2),
-                       (dict(width=0), 1), (dict(S=-1), 1)]:
+                       (dict(width=0), 1), (dict(S=-1), 1), (dict(n=1 << 30, S=1), 2)]:
         assert append(lib, p, **kw) == status, kw
 
 

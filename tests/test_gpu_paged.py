@@ -98,6 +98,8 @@ ATTENTION = [
     (BF16, 128, 48, 2, 64, 1, "dense", [1, 1000, 64]),
     (BF16, 128, 5, 1, 128, 1, "kv", [5000]),
     (BF16, 128, 2, 1, 256, 3, "dense", [0, 0, 3]),
+    (BF16, 128, 64, 1, 16, 1, "dense", [3000, 17]),
+    (BF16, 128, 1, 1, 16, 1, "kv", [20000]),
     (F32, 64, 6, 3, 16, 2, "dense", [1, 0, 15, 16, 17, 63, 64, 65, 300]),
     (F32, 128, 4, 4, 2, 1, "layers", [129, 1000, 1]),
     (F32, 128, 17, 1, 32, 1, "kv", [33, 0, 2049]),
@@ -203,6 +205,32 @@ def test_attention_replays_with_new_lengths_on_another_stream():
     out2, lse2 = api().kvsel_paged_attention(q, c.K, c.V, c.table, c.dlens, stream=side)
     side.synchronize()
     assert torch.equal(out2, out) and torch.equal(lse2, lse)
+
+
+def test_calls_on_two_streams_at_once():
+    """Each call has a workspace of its own: many of them in flight on two streams give what
+    they give alone."""
+    a = api()
+    caches = [Cache([4000 + 300 * i, 77, 0, 900], 16, 1, 2, 128, BF16, seed=20 + i) for i in range(2)]
+    qs = [normal(torch.Generator().manual_seed(30 + i), BF16, 1, 4, 8, 128) for i in range(2)]
+    grown = [ints([n + 1 for n in c.lens]) for c in caches]
+    parents = ints([0, 1, 1, 3])
+
+    def calls(i, stream):
+        c = caches[i]
+        out, lse = a.kvsel_paged_attention(qs[i], c.K, c.V, c.table, c.dlens, stream=stream)
+        return (out, lse, *a.kvsel_pages_update(c.K, c.V, c.table, c.dlens, grown[i], parents=parents,
+                                                stream=stream))
+
+    alone = [calls(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [calls(k % 2, streams[k % 2]) for k in range(40)]
+    torch.cuda.synchronize()
+    assert status() == 0
+    for k, r in enumerate(got):
+        for x, y in zip(r, alone[k % 2]):
+            assert torch.equal(x, y)
 
 
 # ---------------------------------------------------------------------------
