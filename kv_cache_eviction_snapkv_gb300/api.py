@@ -1,7 +1,7 @@
 """Thin Python binding of libkvsel: the C ABI's names, torch tensors in and out.
 
-Argument marshalling only: every step of the selection runs in the library's
-CUDA kernels. Tensors must be CUDA, contiguous, and laid out as ``kvsel.h``
+Argument marshalling only (the paged-cache calls' is native, csrc/binding.cpp):
+every step of the selection runs in the library's CUDA kernels. Tensors must be CUDA, contiguous, and laid out as ``kvsel.h``
 states:
 
     q_win  [layers, S*W, H, D]      K, V  [layers, T, H, D]      (bf16 or fp32)
@@ -451,7 +451,31 @@ def kvsel_cache_lengths(seq_offsets, C: int, g: int):
 # Paged caches
 # ---------------------------------------------------------------------------
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # a stream's handle without the object around it
+_bound = None
+
+
+def _paged():
+    """The native marshalling module, bound to the loaded library."""
+    global _bound
+    lib = _native.lib()
+    if lib is not _bound:
+        try:
+            from . import _kvsel_torch
+        except ImportError as e:
+            raise RuntimeError("_kvsel_torch.so is missing or does not load: build it with "
+                               "`python -m kv_cache_eviction_snapkv_gb300.build`") from e
+        _kvsel_torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "kvsel_paged_append", "kvsel_paged_attention", "kvsel_paged_attention_bytes",
+            "kvsel_paged_compact", "kvsel_pages_update", "kvsel_pages_update_bytes")))
+        _paged.module, _bound = _kvsel_torch, lib
+    return _paged.module
+
+
+def _result(r, where: str):
+    """What a native call returned; a status raises."""
+    if type(r) is int:
+        raise KvselError(r, where)
+    return r
 
 
 @contextlib.contextmanager
@@ -470,72 +494,14 @@ def _on(device: int, stream):
             yield
 
 
-def _elsewhere(device: int, stream) -> bool:
-    """Whether a call on `device` needs `_on` (another device or stream than the current ones)."""
-    return stream is not None or device != torch.cuda.current_device()
-
-
-def _i32(t: torch.Tensor, name: str, device: int) -> int:
-    """Address of a contiguous int32 tensor on `device`."""
-    if t.dtype is not torch.int32 or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on the cache's device")
-    return t.data_ptr()
-
-
-def _opt(t: Optional[torch.Tensor], name: str, device: int) -> Optional[int]:
-    return None if t is None else _i32(t, name, device)
-
-
-def _pool(K: torch.Tensor, V: torch.Tensor) -> _native.KvselPages:
-    shape, stride, code = K.shape, K.stride(), _DTYPES.get(K.dtype)
-    if V.shape != shape or V.dtype is not K.dtype or V.get_device() != K.get_device():
-        raise ValueError("K and V must have one shape, type and device")
-    if not K.is_cuda:
-        raise ValueError("K must be a CUDA tensor")
-    if code is None:
-        raise ValueError("K must be bf16 or fp32")
-    if len(shape) == 4:
-        layers, ls = 1, 0
-        pages, ps, hkv, d = shape
-        pg, s2, s3, s4 = stride
-    elif len(shape) == 5:
-        layers, pages, ps, hkv, d = shape
-        ls, pg, s2, s3, s4 = stride
-    else:
-        raise ValueError("K and V must be [layers, pages, page_size, H_kv, D]")
-    # the stride of a dimension of one entry means nothing
-    if (s4 != 1 and d > 1) or (s3 != d and hkv > 1) or (s2 != hkv * d and ps > 1):
-        raise ValueError("K and V must be dense in their last three dimensions")
-    if V.stride() != stride and any(n > 1 and x != y for n, x, y in zip(shape, stride, V.stride())):
-        raise ValueError("K and V must have the same strides")
-    return _native.KvselPages(layers, pages, ps, hkv, d, code, ls if layers > 1 else 0,
-                              pg if pages > 1 else 0, K.data_ptr(), V.data_ptr())
-
-
-def _workspace(workspace, need: int, K: torch.Tensor) -> torch.Tensor:
-    if workspace is None:
-        if need < 0:
-            raise KvselError(KVSEL_ERR_INVALID_ARG, "workspace")
-        return torch.empty(need, dtype=torch.uint8, device=K.device)
-    if workspace.get_device() != K.get_device() or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    return workspace
-
-
-def _rows_of(t: torch.Tensor, name: str, K: torch.Tensor, layers: int, tokens: int, heads: int,
-             dim: int) -> _native.KvselRows:
-    """kvsel_rows of a [layers, tokens, heads, D] tensor (one layer: 3-D)."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 3:
-        shape, stride = (1, *shape), (0, *stride)
-    if shape != (layers, tokens, heads, dim):
-        raise ValueError(f"{name} must be {(layers, tokens, heads, dim)}, got {tuple(t.shape)}")
-    if t.dtype is not K.dtype or t.get_device() != K.get_device():
-        raise ValueError(f"{name} must have the cache's type and device")
-    ls, ts, hs, es = stride
-    if (heads > 1 and hs != dim) or es != 1:
-        raise ValueError(f"{name} must be dense in its last two dimensions")
-    return _native.KvselRows(t.data_ptr(), ls if layers > 1 else 0, ts if tokens > 1 else 0)
+def _call(name: str, K: torch.Tensor, stream, *args):
+    """A native call on the cache's device and the given (or current) stream."""
+    f = getattr(_paged(), name)
+    device = K.get_device()
+    if device < 0 or (stream is None and device == torch.cuda.current_device()):
+        return _result(f(*args), "kvsel_" + name)      # (a host tensor is refused there)
+    with _on(device, stream):
+        return _result(f(*args), "kvsel_" + name)
 
 
 def kvsel_rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = KVSEL_ROPE_PLAIN,
@@ -557,64 +523,8 @@ def kvsel_paged_append(q, k, v, K, V, cache_pos, positions=None, table=None, seq
     """Norm, rotation and cache rows of new tokens; returns q_out [layers, N, H, D] (None
     without q). q [layers, N, H, D], k, v [layers, N, H_kv, D]: dense in the last two
     dimensions (one layer: 3-D). inv_freq [rot_dim / 2] fp32 (None: no rotation)."""
-    pool = _pool(K, V)
-    dev = K.get_device()
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return kvsel_paged_append(q, k, v, K, V, cache_pos, positions, table, seqs, q_weight,
-                                      k_weight, eps, inv_freq, interleaved, scale, q_out)
-    if q is None and k is None:
-        raise ValueError("q or k and v must be given")
-    if (k is None) != (v is None):
-        raise ValueError("k and v go together")
-    layers, hkv, dim = pool.num_layers, pool.num_kv_heads, pool.head_dim
-    byref = ctypes.byref
-    rq = rk = rv = rope = at = out = None
-    heads = 0
-    if q is not None:
-        n, heads = q.shape[-3], q.shape[-2]
-        rq = byref(_rows_of(q, "q", K, layers, n, heads, dim))
-    else:
-        n = k.shape[-3]
-    if k is not None:
-        rk = byref(_rows_of(k, "k", K, layers, n, hkv, dim))
-        rv = byref(_rows_of(v, "v", K, layers, n, hkv, dim))
-        if cache_pos is None or cache_pos.numel() != n:
-            raise ValueError("cache_pos must have one entry a token")
-        at = _i32(cache_pos, "cache_pos", dev)
-    if inv_freq is not None and inv_freq.numel():
-        if (inv_freq.dtype is not torch.float32 or inv_freq.get_device() != dev or
-                not inv_freq.is_contiguous()):
-            raise ValueError("inv_freq must be a contiguous fp32 tensor on the cache's device")
-        if positions is None or positions.numel() != n:
-            raise ValueError("positions must have one entry a token")
-        rope = byref(_native.KvselRope(2 * inv_freq.numel(), 1 if interleaved else 0,
-                                       inv_freq.data_ptr(), scale))
-    if seqs is not None and seqs.numel() != n:
-        raise ValueError("seqs must have one entry a token")
-    n_seqs = width = 0
-    if table is not None:
-        if table.dim() != 2:
-            raise ValueError("table must be [num_seqs, table_width]")
-        n_seqs, width = table.shape
-    weights = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype is not K.dtype or w.get_device() != dev or
-                              not w.is_contiguous() or w.numel() != layers * dim):
-            raise ValueError(f"{name} must be a contiguous [layers, D] tensor of the cache's type")
-        weights.append(None if w is None else w.data_ptr())
-    if q is not None:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=K.dtype, device=K.device)
-        elif (q_out.shape != q.shape or q_out.get_device() != dev or q_out.dtype is not K.dtype or
-              not q_out.is_contiguous()):
-            raise ValueError("q_out must be contiguous, with q's shape, type and device")
-        out = q_out.data_ptr()
-    _check(_native.lib().kvsel_paged_append(
-        byref(pool), n, heads, rq, rk, rv, rope, weights[0], weights[1], eps,
-        _opt(positions, "positions", dev), n_seqs, _opt(table, "table", dev), width,
-        _opt(seqs, "seqs", dev), at, out, _raw_stream(dev)), "kvsel_paged_append")
-    return q_out if q is not None else None
+    return _call("paged_append", K, stream, q, k, v, K, V, cache_pos, positions, table, seqs,
+                 q_weight, k_weight, eps, inv_freq, interleaved, scale, q_out)
 
 
 def kvsel_paged_attention(q, K, V, table, lens, out=None, lse=None, want_lse: bool = True,
@@ -622,69 +532,15 @@ def kvsel_paged_attention(q, K, V, table, lens, out=None, lse=None, want_lse: bo
     """(out [layers, S, H, D] fp32, lse [layers, S, H] fp32 or None): one query per (layer,
     sequence, query head) over the first lens[b] rows of its pages. q [layers, S, H, D] (one
     layer: 3-D, like the pool 4-D)."""
-    pool = _pool(K, V)
-    dev = K.get_device()
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return kvsel_paged_attention(q, K, V, table, lens, out, lse, want_lse, workspace)
-    shape = q.shape
-    L, S, H, D = shape if len(shape) == 4 else (1, *shape)
-    if (L != pool.num_layers or D != pool.head_dim or q.dtype is not K.dtype or
-            q.get_device() != dev or not q.is_contiguous()):
-        raise ValueError("q must be contiguous [layers, S, H, D] of the cache's layers, D, type and "
-                         "device")
-    if table.dim() != 2 or table.shape[0] != S or lens.numel() != S:
-        raise ValueError("table must be [S, table_width] and lens [S]")
-    if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=K.device)
-    elif (out.dtype is not torch.float32 or out.get_device() != dev or out.shape != shape or
-          not out.is_contiguous()):
-        raise ValueError("out must be a contiguous fp32 tensor of q's shape")
-    if lse is None:
-        if want_lse:
-            lse = torch.empty(shape[:-1], dtype=torch.float32, device=K.device)
-    elif (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != shape[:-1] or
-          not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous fp32 tensor [layers, S, H]")
-    lib = _native.lib()
-    ref = ctypes.byref(pool)
-    ws = _workspace(workspace, lib.kvsel_paged_attention_bytes(ref, S, H), K)
-    _check(lib.kvsel_paged_attention(ref, S, H, q.data_ptr(), _i32(table, "table", dev),
-                                     table.shape[1], _i32(lens, "lens", dev), out.data_ptr(),
-                                     None if lse is None else lse.data_ptr(), ws.data_ptr(),
-                                     ws.nbytes, _raw_stream(dev)), "kvsel_paged_attention")
-    return out, lse
+    return _call("paged_attention", K, stream, q, K, V, table, lens, out, lse, want_lse, workspace)
 
 
 def kvsel_paged_compact(K, V, table, lens, keep_idx, keep_offsets, max_keep: int, ref=None,
                         slot_pos=None, stream=None):
     """slot_pos [layers, keep_rows, H_kv] int32: the cache cut in place to the rows that
     keep_idx [layers, keep_rows, H_kv] names (sequence b's at keep_offsets[b] ..)."""
-    pool = _pool(K, V)
-    dev = K.get_device()
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return kvsel_paged_compact(K, V, table, lens, keep_idx, keep_offsets, max_keep, ref,
-                                       slot_pos)
-    shape = keep_idx.shape
-    L, rows, H = shape if len(shape) == 3 else (1, *shape)
-    if L != pool.num_layers or H != pool.num_kv_heads:
-        raise ValueError("keep_idx must be [layers, keep_rows, H_kv]")
-    S, width = table.shape
-    if lens.numel() != S or keep_offsets.numel() != S + 1:
-        raise ValueError("lens must have S entries and keep_offsets S + 1")
-    if ref is not None and ref.numel() != pool.num_pages:
-        raise ValueError("ref must have one entry a page")
-    if slot_pos is None:
-        slot_pos = torch.empty(shape, dtype=torch.int32, device=K.device)
-    elif slot_pos.shape != shape:
-        raise ValueError("slot_pos must have keep_idx's shape")
-    _check(_native.lib().kvsel_paged_compact(
-        ctypes.byref(pool), S, _i32(table, "table", dev), width, _i32(lens, "lens", dev),
-        _i32(keep_idx, "keep_idx", dev), rows, _i32(keep_offsets, "keep_offsets", dev), max_keep,
-        _opt(ref, "ref", dev), _i32(slot_pos, "slot_pos", dev), _raw_stream(dev)),
-        "kvsel_paged_compact")
-    return slot_pos
+    return _call("paged_compact", K, stream, K, V, table, lens, keep_idx, keep_offsets,
+                 int(max_keep), ref, slot_pos)
 
 
 def kvsel_pages_update(K, V, table, lens, new_lens, parents=None, table_out=None, ref=None,
@@ -692,35 +548,8 @@ def kvsel_pages_update(K, V, table, lens, new_lens, parents=None, table_out=None
     """(table_out [num_out, table_width], ref [pages], free_pages [1]), int32: the tables of the
     next step's sequences; new sequence b goes on from old sequence parents[b] (-1: none; None:
     b) and holds pages for new_lens[b] rows."""
-    pool = _pool(K, V)
-    dev = K.get_device()
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return kvsel_pages_update(K, V, table, lens, new_lens, parents, table_out, ref,
-                                      free_pages, workspace)
-    n_in, width = table.shape
-    n_out = new_lens.numel()
-    if lens.numel() != n_in or (parents is not None and parents.numel() != n_out):
-        raise ValueError("lens must have one entry an old sequence, parents one a new one")
-    device = K.device
-    if table_out is None:
-        table_out = torch.empty((n_out, width), dtype=torch.int32, device=device)
-    if ref is None:
-        ref = torch.empty(pool.num_pages, dtype=torch.int32, device=device)
-    if free_pages is None:
-        free_pages = torch.empty(1, dtype=torch.int32, device=device)
-    if (table_out.shape != (n_out, width) or ref.numel() != pool.num_pages or
-            free_pages.numel() != 1):
-        raise ValueError("table_out must be [num_out, table_width], ref [pages], free_pages [1]")
-    lib = _native.lib()
-    p = ctypes.byref(pool)
-    ws = _workspace(workspace, lib.kvsel_pages_update_bytes(p, n_out), K)
-    _check(lib.kvsel_pages_update(p, n_in, _i32(table, "table", dev), width, _i32(lens, "lens", dev),
-                                  n_out, _opt(parents, "parents", dev),
-                                  _i32(new_lens, "new_lens", dev), _i32(table_out, "table_out", dev),
-                                  _i32(ref, "ref", dev), _i32(free_pages, "free_pages", dev),
-                                  ws.data_ptr(), ws.nbytes, _raw_stream(dev)), "kvsel_pages_update")
-    return table_out, ref, free_pages
+    return _call("pages_update", K, stream, K, V, table, lens, new_lens, parents, table_out, ref,
+                 free_pages, workspace)
 
 
 def kvsel_device_status(stream=None) -> int:
