@@ -518,7 +518,7 @@ kvsel_status kvsel_paged_compact(const kvsel_pages* pages, int32_t num_seqs, con
  *   are -1, NO_PAGES is recorded).
  * workspace: kvsel_pages_update_bytes(pages, num_out) bytes, 16-byte aligned. Rules:
  * INVALID_ARG for negative counts, a workspace that is too small or misaligned,
- * parents NULL with num_in != num_out; UNSUPPORTED for num_out * table_width >=
+ * parents NULL with num_in != num_out > 0; UNSUPPORTED for num_out * table_width >=
  * 2^31. Device status: BAD_INDEX for a parent, length or page out of range (such a
  * sequence becomes empty; such a page's entry becomes -1).
  * Asynchronous; capturable. */

@@ -267,7 +267,7 @@ kvsel_status kvsel_pages_update(const kvsel_pages* pages, int32_t num_in, const 
   if ((st = check_table(a.pv, num_in, table, table_width))) return st;
   if ((st = check_table(a.pv, num_out, table_out, table_width))) return st;
   if ((num_in > 0 && !lens) || (num_out > 0 && !new_lens) || (a.pv.num_pages > 0 && !ref) ||
-      (!parents && num_in != num_out))
+      (!parents && num_out > 0 && num_in != num_out))
     return KVSEL_ERR_INVALID_ARG;
   if (num_in > 0 && num_out > 0) {
     const int32_t* in_end = table + (int64_t)num_in * table_width;

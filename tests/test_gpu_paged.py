@@ -133,6 +133,49 @@ def test_attention_large_scores_and_many_sequences():
     check_attention(c, q, out, lse)
 
 
+def test_attention_of_the_most_sequences():
+    """8192 sequences, most of them empty or of a few rows, and layers."""
+    c = Cache([(i * 7) % 5 if i % 3 else 0 for i in range(8192)], 2, 2, 1, 64, F32, seed=13)
+    q = normal(torch.Generator().manual_seed(14), F32, 2, 8192, 1, 64)
+    out, lse = api().kvsel_paged_attention(q, c.K, c.V, c.table, c.dlens)
+    assert status() == 0
+    check_attention(c, q, out, lse)
+    with pytest.raises(api().KvselError) as e:
+        api().kvsel_paged_attention(torch.zeros((2, 8193, 1, 64), device=DEV), c.K, c.V,
+                                    torch.zeros((8193, 1), dtype=torch.int32, device=DEV),
+                                    torch.zeros(8193, dtype=torch.int32, device=DEV))
+    assert e.value.status == api().KVSEL_ERR_UNSUPPORTED
+
+
+def test_calls_on_nothing():
+    """No sequences, no tokens, no pages: nothing is done, and update frees every page."""
+    a = api()
+    c = Cache([20, 5], 16, 1, 2, 64, BF16, seed=15)
+    none = ints([])
+    empty = torch.zeros((0, c.table.shape[1]), dtype=torch.int32, device=DEV)
+    out, lse = a.kvsel_paged_attention(torch.zeros((1, 0, 4, 64), dtype=BF16, device=DEV), c.K, c.V, empty,
+                                       none)
+    assert out.shape == (1, 0, 4, 64) and lse.shape == (1, 0, 4)
+    q = a.kvsel_paged_append(torch.zeros((0, 4, 64), dtype=BF16, device=DEV), None, None, c.K, c.V, None)
+    assert q.shape == (0, 4, 64)
+    t, ref, free = a.kvsel_pages_update(c.K, c.V, c.table, c.dlens, none, parents=none)
+    assert t.shape[0] == 0 and not ref.any() and free.item() == c.P
+    t, ref, free = a.kvsel_pages_update(c.K, c.V, empty, none, ints([17, 0, 1]), parents=ints([-1, -1, -1]))
+    assert t[:, :2].tolist() == [[0, 1], [-1, -1], [2, -1]] and free.item() == c.P - 3
+    nothing = torch.zeros((1, 0, 16, 2, 64), dtype=BF16, device=DEV)
+    assert status() == 0
+    out, lse = a.kvsel_paged_attention(torch.ones((1, 1, 2, 64), dtype=BF16, device=DEV), nothing, nothing,
+                                       ints([[0]]), ints([3]))
+    assert status() == a.KVSEL_ERR_BAD_INDEX
+    assert not out.any() and bool(torch.isneginf(lse).all())
+    t, ref, free = a.kvsel_pages_update(nothing, nothing, ints([[-1]]), ints([0]), ints([3]))
+    assert status() == a.KVSEL_ERR_NO_PAGES
+    assert t.tolist() == [[-1]] and free.item() == -1
+    pos = a.kvsel_paged_compact(c.K, c.V, c.table, c.dlens, torch.zeros((1, 0, 2), dtype=torch.int32,
+                                                                        device=DEV), ints([0, 0, 0]), 4)
+    assert pos.shape == (1, 0, 2) and status() == 0
+
+
 def test_attention_agrees_with_the_packed_call():
     """A packed cache is a pool of one-row pages; both calls read it alike."""
     gen = torch.Generator().manual_seed(9)
@@ -384,6 +427,7 @@ COMPACT = [
     (F32, 64, 1, 8, 3, "layers", [700, 3], [256, 2]),
     (F32, 128, 2, 64, 1, "dense", [3000], [1033]),
     (BF16, 128, 8, 32, 1, "dense", [21000], [16500]),
+    (BF16, 64, 1, 16, 1, "dense", [33001], [32768]),
 ]
 
 
