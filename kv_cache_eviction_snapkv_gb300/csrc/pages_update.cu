@@ -32,7 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 8;                 // of the cluster, at most
 constexpr int kColumns = 128;              // table columns a warp counts at a time
 constexpr int kItems = 4;                  // such pieces that it has in flight
-constexpr int kTiles = 8;                  // of a page a thread, numbered together
+constexpr int kTiles = 4;                  // of a page a thread, numbered together
 static_assert(kTiles * kWarps <= kThreads, "a thread a count");
 constexpr int kPiece = 32768;              // bytes a block copies at a time
 constexpr int kSharedSeqs = 2048;          // sequences whose records fit shared memory
@@ -104,7 +104,7 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
 __global__ void __launch_bounds__(kThreads)
     pages_table_kernel(const __grid_constant__ PagesUpdateArgs a, int blocks, int p_run,
                        uint32_t run_inverse, bool shared_pages) {
-  extern __shared__ int smem[];          // counts [p_run], lowest users [p_run]
+  extern __shared__ __align__(16) int smem[];  // counts [p_run], lowest users [p_run]
   __shared__ Taken shared_take[kSharedSeqs];
   __shared__ int warp_sums[kWarps], tile_sums[kTiles * kWarps];
   __shared__ int free_of[kBlocks];       // every block's, written by their owners
@@ -141,27 +141,39 @@ __global__ void __launch_bounds__(kThreads)
       *owner = owners + page;
     }
   };
-  for (int i = tid; i < p1 - p0; i += kThreads) {
-    own_count[i] = 0;
-    own_owner[i] = 0x7fffffff;
+  if (shared_pages) {
+    for (int i = tid; i < p_run / 4; i += kThreads) {
+      reinterpret_cast<int4*>(own_count)[i] = make_int4(0, 0, 0, 0);
+      reinterpret_cast<int4*>(own_owner)[i] = make_int4(0x7fffffff, 0x7fffffff, 0x7fffffff, 0x7fffffff);
+    }
+  } else {
+    for (int i = tid; i < p1 - p0; i += kThreads) {
+      own_count[i] = 0;
+      own_owner[i] = 0x7fffffff;
+    }
   }
-  for (int b = tid; b < a.num_out; b += kThreads) take[b] = taken(a, b);
+  const int64_t W = a.table_width;
+  int started = -1;                      // entry of this thread's first sequence's started page
+  for (int b = tid; b < a.num_out; b += kThreads) {
+    const Taken t = taken(a, b);
+    take[b] = t;
+    if (b == tid && (t.rows & mask)) started = __ldg(a.table + t.row * W + (t.rows >> shift));
+  }
   if (gtid == 0) *n_copies = 0;
   barrier();
 
   // whole uses, and the lowest user of every started page
-  const int64_t W = a.table_width;
-  const int chunks = (a.table_width + kColumns - 1) / kColumns;
-  const int64_t items = (int64_t)a.num_out * chunks;
+  const uint32_t chunks = (a.table_width + kColumns - 1) / kColumns;
+  const uint32_t items = (uint32_t)a.num_out * chunks;           // < 2^31, as num_out * table_width
   constexpr int kCols = kColumns / 32;
-  for (int64_t it0 = gtid >> 5; it0 < items; it0 += all / 32 * kItems) {
+  for (uint32_t it0 = gtid >> 5; it0 < items; it0 += all / 32 * kItems) {
     int page[kItems][kCols], b[kItems], c0[kItems], whole[kItems];
 #pragma unroll
     for (int j = 0; j < kItems; ++j) {
-      const int64_t it = it0 + j * (all / 32);
+      const uint32_t it = it0 + j * (all / 32);
       const bool in = it < items;
-      b[j] = !in ? 0 : chunks == 1 ? (int)it : (int)(it / chunks);
-      c0[j] = in ? (int)(it - (int64_t)b[j] * chunks) * kColumns + lane : 0;
+      b[j] = in ? (int)(it / chunks) : 0;
+      c0[j] = in ? (int)(it - b[j] * chunks) * kColumns + lane : 0;
       const Taken t = take[b[j]];
       whole[j] = t.rows >> shift;
       const int last = in ? whole[j] + (t.rows & mask ? 1 : 0) : 0;      // columns in use
@@ -196,8 +208,8 @@ __global__ void __launch_bounds__(kThreads)
     if (b < a.num_out) {
       const Taken t = take[b];
       if (t.rows & mask) {
-        const int src = checked_page(a.pv, a.table + t.row * W, t.rows >> shift, a.status);
-        if (src >= 0) {
+        const int src = bb == 0 ? started : __ldg(a.table + t.row * W + (t.rows >> shift));
+        if (src >= 0 && src < P) {       // (reported above if not)
           int *count, *owner;
           state_of(src, &count, &owner);
           keeps = *count == 0 && *owner == b;
@@ -250,7 +262,27 @@ __global__ void __launch_bounds__(kThreads)
   int nfree;
   {
     int n = 0;
-    if (shared_pages) {
+    if (shared_pages && (reinterpret_cast<uintptr_t>(a.ref) & 15) == 0) {
+      const int end = p1 - p0;           // p0 is a multiple of 4
+      for (int i = 4 * tid; i < end; i += 4 * kThreads) {
+        const int4 c = *reinterpret_cast<const int4*>(own_count + i);
+        const int4 o = *reinterpret_cast<const int4*>(own_owner + i);
+        const int4 r = make_int4(c.x ? c.x : o.x != 0x7fffffff, c.y ? c.y : o.y != 0x7fffffff,
+                                 c.z ? c.z : o.z != 0x7fffffff, c.w ? c.w : o.w != 0x7fffffff);
+        if (i + 4 <= end) {
+          n += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+          *reinterpret_cast<int4*>(a.ref + p0 + i) = r;
+        } else {
+          const int left[3] = {r.x, r.y, r.z};
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            if (i + k < end) {
+              n += left[k] == 0;
+              a.ref[p0 + i + k] = left[k];
+            }
+        }
+      }
+    } else if (shared_pages) {
       for (int i = tid; i < p1 - p0; i += kThreads) {
         const int c = own_count[i];
         const bool started = own_owner[i] != 0x7fffffff;
@@ -382,7 +414,7 @@ cudaError_t launch_pages_update(const PagesUpdateArgs& a) {
   const int64_t items = (int64_t)a.num_out * ((a.table_width + kColumns - 1) / kColumns);
   const bool one = a.pv.num_pages <= kSharedPages / 4 && items <= 4 * kWarps;
   const int blocks = one ? 1 : kBlocks;
-  const int p_run = (int)std::max<int64_t>(((int64_t)a.pv.num_pages + blocks - 1) / blocks, 1024);
+  const int p_run = (int)std::max<int64_t>((((int64_t)a.pv.num_pages + blocks - 1) / blocks + 3) & ~int64_t(3), 1024);
   const bool shared_pages = p_run <= kSharedPages;
   const uint32_t run_inverse = (uint32_t)(((uint64_t(1) << 40) + p_run - 1) / p_run);
   static_assert(kSharedPages * 8 + kSharedSeqs * 16 + 8 * 1024 <= 227 * 1024, "fits shared memory");

@@ -543,7 +543,11 @@ def test_update_many_sequences_and_pages():
     c = Cache(lens, 16, 1, 1, 64, BF16, seed=3, spare=9000)
     parents = [int(x) for x in rng.integers(-1, 1500, size=1700)]
     new = [min(400, lens[p] + 1 if p >= 0 else 40) for p in parents]
-    check_update(c, parents, new)
+    args = (c.K, c.V, c.table, c.dlens, ints(new), ints(parents))
+    ref = check_update(c, parents, new)
+    odd = torch.empty(c.P + 1, dtype=torch.int32, device=DEV)[1:]      # not on a 16-byte boundary
+    _, got, _ = api().kvsel_pages_update(*args, ref=odd)
+    assert status() == 0 and got is odd and got.tolist() == ref
 
 
 def test_update_more_sequences_and_pages_than_shared_memory_holds():
