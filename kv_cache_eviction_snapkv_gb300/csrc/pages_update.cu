@@ -30,8 +30,8 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 8;                 // of the cluster, at most
-constexpr int kColumns = 128;              // table columns a warp counts at a time
-constexpr int kItems = 4;                  // such pieces that it has in flight
+constexpr int kColumns = 256;              // table columns a warp counts at a time
+constexpr int kItems = 3;                  // such pieces that it has in flight
 constexpr int kTiles = 4;                  // of a page a thread, numbered together
 static_assert(kTiles * kWarps <= kThreads, "a thread a count");
 constexpr int kPiece = 32768;              // bytes a block copies at a time
@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(kThreads)
         if (src >= 0 && src < P) {       // (reported above if not)
           int *count, *owner;
           state_of(src, &count, &owner);
-          keeps = *count == 0 && *owner == b;
+          const int n = *count, lowest = *owner;       // both on their way at once
+          keeps = n == 0 && lowest == b;
         }
       }
       fresh = ((t.want + mask) >> shift) - (t.rows >> shift) - (keeps ? 1 : 0);
