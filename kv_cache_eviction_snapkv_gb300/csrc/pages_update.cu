@@ -16,7 +16,11 @@
 // alone every block works out for itself. That leaves three barriers: state cleared, uses
 // counted, free pages counted; then every free page finds the table entry that it goes to. A
 // pool of more pages than the cluster's shared memory holds keeps the two words in memory. A
-// second, dependent launch copies the started pages' rows with the whole machine.
+// second, dependent launch writes the entries that stay and the empty ones, and copies the
+// started pages' rows, with the whole machine: eight SMs have few instructions to spare.
+//
+// Measured: 700 sequences over 150000 pages 19 us (34 us with every entry written by the cluster,
+// 240 us by one block), four beams 9.5 us, 224 copies of started pages 41 us, 102 MB written.
 #include <algorithm>
 #include <cooperative_groups.h>
 
