@@ -362,7 +362,7 @@ kvsel_status kvsel_cache_lengths(const kvsel_shape* shape, int32_t C, int32_t g,
  * num_pages < 0, a stride below a page's elements), NULL pointers where data is
  * needed, K or V or a stride not 32-byte aligned; UNSUPPORTED for D not in
  * {64, 128}, a page_size that is no power of two, a pool of 2^31 or more rows or
- * 128 GiB or more per layer, a table of 2^31 or more rows per sequence. A packed
+ * 128 GiB or more per layer, a table of 2^30 or more rows per sequence. A packed
  * cache [num_layers][T][H_kv][D] is a pool of T pages of one row.
  * ------------------------------------------------------------------------- */
 typedef struct kvsel_pages {

@@ -57,7 +57,8 @@ kvsel_status check_table(const PagedView& v, int num_seqs, const int32_t* table,
   if (num_seqs < 0) return KVSEL_ERR_INVALID_ARG;
   if (num_seqs == 0) return KVSEL_OK;
   if (width < 1 || !table) return KVSEL_ERR_INVALID_ARG;
-  if ((int64_t)width * v.page_size > 0x7fffffffLL || (int64_t)num_seqs * width > 0x7fffffffLL)
+  // (the kernels' int arithmetic has room above the last row and column)
+  if ((int64_t)width * v.page_size >= (int64_t(1) << 30) || (int64_t)num_seqs * width > 0x7fffffffLL)
     return KVSEL_ERR_UNSUPPORTED;
   return KVSEL_OK;
 }

@@ -78,6 +78,16 @@ def test_pool_rules_hold_for_every_call(lib, change, status):
     assert update(lib, p) == status
 
 
+def test_tables_of_too_many_rows(lib):
+    """2^30 rows a sequence, whatever the page size."""
+    for ps, width in ((1, 1 << 30), (16, 1 << 26), (1024, 1 << 20)):
+        p = pool(page_size=ps)
+        assert attention(lib, p, S=1, width=width) == 2
+        assert append(lib, p, width=width, S=1, n=1) == 2
+        assert compact(lib, p, S=1, width=width) == 2
+        assert update(lib, p, n_in=1, n_out=1, width=width, ws_bytes=1 << 40) == 2
+
+
 def test_null_pool(lib):
     assert lib.kvsel_paged_attention(None, 1, 1, P, P, 1, P, P, None, P, 1 << 30, None) == 1
     assert lib.kvsel_paged_attention_bytes(None, 1, 1) == -1
