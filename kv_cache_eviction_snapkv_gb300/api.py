@@ -452,30 +452,22 @@ def kvsel_cache_lengths(seq_offsets, C: int, g: int):
 # ---------------------------------------------------------------------------
 
 _bound = None
+_native_paged = None
 
 
-def _paged():
-    """The native marshalling module, bound to the loaded library."""
-    global _bound
+def _bind():
+    """Loads the native marshalling module and gives it the loaded library's entry points."""
+    global _bound, _native_paged
     lib = _native.lib()
-    if lib is not _bound:
-        try:
-            from . import _kvsel_torch
-        except ImportError as e:
-            raise RuntimeError("_kvsel_torch.so is missing or does not load: build it with "
-                               "`python -m kv_cache_eviction_snapkv_gb300.build`") from e
-        _kvsel_torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
-            "kvsel_paged_append", "kvsel_paged_attention", "kvsel_paged_attention_bytes",
-            "kvsel_paged_compact", "kvsel_pages_update", "kvsel_pages_update_bytes")))
-        _paged.module, _bound = _kvsel_torch, lib
-    return _paged.module
-
-
-def _result(r, where: str):
-    """What a native call returned; a status raises."""
-    if type(r) is int:
-        raise KvselError(r, where)
-    return r
+    try:
+        from . import _kvsel_torch
+    except ImportError as e:
+        raise RuntimeError("_kvsel_torch.so is missing or does not load: build it with "
+                           "`python -m kv_cache_eviction_snapkv_gb300.build`") from e
+    _kvsel_torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        "kvsel_paged_append", "kvsel_paged_attention", "kvsel_paged_attention_bytes",
+        "kvsel_paged_compact", "kvsel_pages_update", "kvsel_pages_update_bytes")))
+    _bound, _native_paged = lib, _kvsel_torch
 
 
 @contextlib.contextmanager
@@ -496,12 +488,18 @@ def _on(device: int, stream):
 
 def _call(name: str, K: torch.Tensor, stream, *args):
     """A native call on the cache's device and the given (or current) stream."""
-    f = getattr(_paged(), name)
+    if _bound is None or _bound is not _native._lib:
+        _bind()
+    f = getattr(_native_paged, name)
     device = K.get_device()
     if device < 0 or (stream is None and device == torch.cuda.current_device()):
-        return _result(f(*args), "kvsel_" + name)      # (a host tensor is refused there)
-    with _on(device, stream):
-        return _result(f(*args), "kvsel_" + name)
+        r = f(*args)                                   # (a host tensor is refused there)
+    else:
+        with _on(device, stream):
+            r = f(*args)
+    if type(r) is int:
+        raise KvselError(r, "kvsel_" + name)
+    return r
 
 
 def kvsel_rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = KVSEL_ROPE_PLAIN,
