@@ -578,16 +578,16 @@ __global__ void __launch_bounds__(kThreads, Step<T, D, NT>::kBlocks)
 }
 
 // Joins the split instances' pieces. An instance that spans the parts first .. last is joined by
-// the blocks first .. last, its heads shared out among them. A block's warps share its heads (of
-// the instance that goes on in its part and of the one that begins there), and the pieces of a
-// head where there are fewer heads than warps; every warp keeps a maximum of its own, so that one
-// round of loads does where the pieces are few.
+// the blocks first .. last, which share out its heads, or quarters of its heads' values. A block's warps share its items (of the instance that goes on in
+// its part and of the one that begins there), and the pieces of an item where there are fewer
+// items than warps; within a warp, as many lanes as the item's values need take a piece. Every
+// lane group keeps a maximum of its own, so that one pass over the pieces does.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __grid_constant__ PagedAttnArgs a,
-                                                                  const __grid_constant__ AttnGeom gm) {
-  constexpr int kJoinWarps = kJoinThreads / 32, E = D / 32, kAhead = 4;
+                                                                     const __grid_constant__ AttnGeom gm) {
+  constexpr int kJoinWarps = kJoinThreads / 32, kAhead = 4;
   __shared__ float maxs[kJoinWarps], sums[kJoinWarps];
-  __shared__ __align__(16) float vals[kJoinWarps][D];
+  __shared__ float4 vals[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = gm.grid * kWarps;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -595,39 +595,49 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __gri
   const float* acc = reinterpret_cast<const float*>(a.ws + ws_acc(warps, gm.heads));
   const SplitInfo* infos = reinterpret_cast<const SplitInfo*>(a.ws) + 2 * blockIdx.x;
   const SplitInfo on = infos[0], begun = infos[1];
-  // heads of either that are this block's: its place among the parts, then every n-th
+  // log2 of the parts that a head's values are joined in: four where the pieces are many (24
+  // heads of 1216 pieces: 41 us for the call, 71 without), one where they are few (0.5 us less);
+  // and the items that are this block's: its place among the instance's blocks, then every n-th
+  auto slices = [](const SplitInfo& i) {
+    const int n = i.last - i.first + 1;
+    return n >= 64 && n >= 4 * i.heads ? 2 : 0;
+  };
   auto share = [&](const SplitInfo& i) {
-    const int n = i.last - i.first + 1, at = blockIdx.x - i.first;
-    return i.first_head < 0 || at >= i.heads ? 0 : (i.heads - at + n - 1) / n;
+    if (i.first_head < 0) return 0;           // nothing else of it is written
+    const int n = i.last - i.first + 1, at = (int)blockIdx.x - i.first;
+    const int items = i.heads << slices(i);
+    return at >= items ? 0 : (items - at + n - 1) / n;
   };
   const int count0 = share(on), count = count0 + share(begun);
   if (count == 0) return;
-  int per = kJoinWarps;                       // warps a head: a power of two
+  int per = kJoinWarps;                       // warps an item: a power of two
   while (per > 1 && per * count > kJoinWarps) per >>= 1;
   const int sub = warp & (per - 1);
   for (int c0 = 0; c0 < count; c0 += kJoinWarps / per) {
     const int c = c0 + warp / per;
     const SplitInfo& info = c < count0 ? on : begun;
-    const int n = info.last - info.first + 1;
-    const int h = (int)blockIdx.x - info.first + (c < count0 ? c : c - count0) * n;
-    float mx = -INFINITY, sum = 0.f, v[E] = {};
+    const int n = info.last - info.first + 1, shift = slices(info);
+    const int item = (int)blockIdx.x - info.first + (c < count0 ? c : c - count0) * n;
+    const int lane_shift = (D == 128 ? 5 : 4) - shift;         // lanes a piece: 4 values each
+    const int h = item >> shift, lanes = 1 << lane_shift;
+    const int place = lane & (lanes - 1), groups = 32 >> lane_shift, grp = lane >> lane_shift;
+    const int d = ((item & ((1 << shift) - 1)) * lanes + place) * 4;
+    float mx = -INFINITY, sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < count) {
-      for (int i0 = sub; i0 < n; i0 += per * kAhead) {
+      const int step = per * groups;
+      for (int i0 = sub * groups + grp; i0 < n; i0 += step * kAhead) {
         float2 y[kAhead];
-        float w[kAhead][E];
+        float4 w[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const int i = i0 + k * per;
+          const int i = i0 + k * step;
           const int64_t at = ((int64_t)(info.first + i) * 2 + (i == 0 ? 1 : 0)) * gm.heads + h;
           y[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int e = 0; e < E; ++e) w[k][e] = 0.f;
+          w[k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (i < n) {
             y[k] = ml[at];
-            if constexpr (E == 4)
-              *reinterpret_cast<float4*>(w[k]) = *reinterpret_cast<const float4*>(acc + at * D + lane * E);
-            else
-              *reinterpret_cast<float2*>(w[k]) = *reinterpret_cast<const float2*>(acc + at * D + lane * E);
+            w[k] = *reinterpret_cast<const float4*>(acc + at * D + d);
           }
         }
         float top = mx;
@@ -636,53 +646,67 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __gri
         const float ref = top == -INFINITY ? 0.f : top, f = ex2(mx - ref);
         mx = top;
         sum *= f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= f;
+        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           const float p = ex2(y[k].x - ref);        // of -inf: 0; a NaN sum stays NaN
           sum = fmaf(y[k].y, p, sum);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] = fmaf(w[k][e], p, v[e]);
+          v = make_float4(fmaf(w[k].x, p, v.x), fmaf(w[k].y, p, v.y), fmaf(w[k].z, p, v.z),
+                          fmaf(w[k].w, p, v.w));
         }
       }
     }
-    __syncthreads();                          // the heads before have been read
+    // the lane groups' results, added in pairs
+    for (int off = lanes; off < 32; off <<= 1) {
+      const float mo = __shfl_xor_sync(0xffffffffu, mx, off), so = __shfl_xor_sync(0xffffffffu, sum, off);
+      const float4 vo = make_float4(__shfl_xor_sync(0xffffffffu, v.x, off), __shfl_xor_sync(0xffffffffu, v.y, off),
+                                    __shfl_xor_sync(0xffffffffu, v.z, off), __shfl_xor_sync(0xffffffffu, v.w, off));
+      const float top = fmaxf(mx, mo), ref = top == -INFINITY ? 0.f : top;
+      const float f = ex2(mx - ref), fo = ex2(mo - ref);
+      mx = top;
+      sum = sum * f + so * fo;
+      v = make_float4(v.x * f + vo.x * fo, v.y * f + vo.y * fo, v.z * f + vo.z * fo, v.w * f + vo.w * fo);
+    }
+    __syncthreads();                          // the items before have been read
     if (lane == 0) {
       maxs[warp] = mx;
       sums[warp] = sum;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) vals[warp][lane * E + e] = v[e];
+    if (grp == 0) vals[warp][place] = v;
     __syncthreads();
-    if (sub != 0 || c >= count) continue;
+    if (sub != 0 || c >= count || grp != 0) continue;
     float top = mx;
     for (int w = 1; w < per; ++w) top = fmaxf(top, maxs[warp + w]);
     const float ref = top == -INFINITY ? 0.f : top;
-    float total = 0.f, r[E] = {};
+    float total = 0.f;
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int w = 0; w < per; ++w) {
       const float f = ex2(maxs[warp + w] - ref);
+      const float4 x = vals[warp + w][place];
       total = fmaf(sums[warp + w], f, total);
-#pragma unroll
-      for (int e = 0; e < E; ++e) r[e] = fmaf(vals[warp + w][lane * E + e], f, r[e]);
+      r = make_float4(fmaf(x.x, f, r.x), fmaf(x.y, f, r.y), fmaf(x.z, f, r.z), fmaf(x.w, f, r.w));
     }
-    bool bad = !finite_f(total);
-    float* out = a.out + (info.first_head + h) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      r[e] = total == 0.f ? 0.f : r[e] / total;
-      bad |= !finite_f(r[e]);
-      out[e] = r[e];
-    }
-    if (lane == 0 && a.lse)
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    r = make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
+    *reinterpret_cast<float4*>(a.out + (info.first_head + h) * D + d) = r;
+    if (d == 0 && a.lse)
       a.lse[info.first_head + h] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
-    if (bad) record_status(a.status, KVSEL_ERR_NONFINITE);
+    if (!finite_f(total) || !finite_f(r.x) || !finite_f(r.y) || !finite_f(r.z) || !finite_f(r.w))
+      record_status(a.status, KVSEL_ERR_NONFINITE);
   }
 }
 
-// Tiles of 8 heads a warp: two in bf16 once a group has more than 8 (a row's fragments then
-// serve two products); fp32's split fragments leave no registers for that.
-int head_tiles(const PagedView& pv, int G) { return pv.dtype == KVSEL_BF16 && G > 8 ? 2 : 1; }
+// Tiles of 8 heads a warp: in bf16 up to three (a row's fragments then serve three products), as
+// many as read the rows the fewest times (24 heads a group: 149 us with three, where two tiles
+// read the rows twice in 200); fp32's split fragments leave registers for one.
+int head_tiles(const PagedView& pv, int G) {
+  if (pv.dtype == KVSEL_F32) return 1;
+  int best = 1;
+  auto reads = [&](int nt) { return (G + 8 * nt - 1) / (8 * nt); };
+  for (int nt = 2; nt <= 3; ++nt)
+    if (reads(nt) < reads(best)) best = nt;
+  return best;
+}
 
 template <typename T, int D, int NT>
 int smem_bytes(int S) {
@@ -693,9 +717,9 @@ int smem_bytes(int S) {
 AttnGeom geometry(const PagedView& pv, int H, int sm_count) {
   AttnGeom gm;
   gm.G = H / pv.Hkv;
-  const int heads = 8 * head_tiles(pv, gm.G);
-  gm.heads = gm.G < heads ? gm.G : heads;
-  gm.HG = (gm.G + gm.heads - 1) / gm.heads;
+  const int most = 8 * head_tiles(pv, gm.G);
+  gm.HG = (gm.G + most - 1) / most;
+  gm.heads = (gm.G + gm.HG - 1) / gm.HG;
   gm.grid = sm_count * (pv.dtype == KVSEL_F32 && pv.D == 128 ? Step<float, 128, 1>::kBlocks
                                                              : Step<__nv_bfloat16, 128, 1>::kBlocks);
   return gm;
@@ -735,11 +759,15 @@ int64_t paged_attention_ws(const PagedView& pv, int S, int H, int sm_count) {
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a) {
   const AttnGeom gm = geometry(a.pv, a.H, a.sm_count);
-  const bool two = head_tiles(a.pv, gm.G) == 2;
+  const int nt = head_tiles(a.pv, gm.G);
   if (a.pv.dtype == KVSEL_BF16) {
     if (a.pv.D == 128)
-      return two ? launch<__nv_bfloat16, 128, 2>(a, gm) : launch<__nv_bfloat16, 128, 1>(a, gm);
-    return two ? launch<__nv_bfloat16, 64, 2>(a, gm) : launch<__nv_bfloat16, 64, 1>(a, gm);
+      return nt == 3   ? launch<__nv_bfloat16, 128, 3>(a, gm)
+             : nt == 2 ? launch<__nv_bfloat16, 128, 2>(a, gm)
+                       : launch<__nv_bfloat16, 128, 1>(a, gm);
+    return nt == 3   ? launch<__nv_bfloat16, 64, 3>(a, gm)
+           : nt == 2 ? launch<__nv_bfloat16, 64, 2>(a, gm)
+                     : launch<__nv_bfloat16, 64, 1>(a, gm);
   }
   return a.pv.D == 128 ? launch<float, 128, 1>(a, gm) : launch<float, 64, 1>(a, gm);
 }
