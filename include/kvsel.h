@@ -448,7 +448,7 @@ kvsel_status kvsel_paged_append(const kvsel_pages* pages, int32_t num_tokens, in
 
 /* kvsel_decode_attention over a paged cache: one query per (layer, sequence,
  * query head) attends to the first lens[b] rows of its sequence. q
- * [num_layers][num_seqs][num_heads][D] (the pool's dtype, 32-byte aligned),
+ * [num_layers][num_seqs][num_heads][D] (the pool's dtype, 16-byte aligned),
  * query head h reads cache head h / (num_heads / H_kv). out
  * [num_layers][num_seqs][num_heads][D] fp32 (16-byte aligned), lse
  * [num_layers][num_seqs][num_heads] fp32 natural log, or NULL. A sequence of

@@ -195,7 +195,7 @@ kvsel_status kvsel_paged_attention(const kvsel_pages* pages, int32_t num_seqs, i
   if (num_seqs == 0) return KVSEL_OK;
   if ((int64_t)num_seqs * table_width > (int64_t(1) << 34) / a.pv.page_size)
     return KVSEL_ERR_UNSUPPORTED;
-  if (!q || !lens || !out || misaligned(q, kRowUnit) || misaligned(out, 16))
+  if (!q || !lens || !out || misaligned(q, 16) || misaligned(out, 16))
     return KVSEL_ERR_INVALID_ARG;
   DeviceInfo d;
   if ((st = device_info(&d))) return st;

@@ -250,6 +250,44 @@ def test_attention_replays_with_new_lengths_on_another_stream():
     assert torch.equal(out2, out) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("dtype,D,H,Hkv", [(BF16, 128, 24, 1), (F32, 64, 6, 2), (F32, 128, 9, 1)])
+def test_workspaces_of_the_least_size(dtype, D, H, Hkv):
+    """Both calls stay within the bytes that they ask for, whatever lies in them before, and a
+    byte less is refused; q on a 16-byte boundary only."""
+    import ctypes
+    from kv_cache_eviction_snapkv_gb300 import _native
+    a = api()
+    c = Cache([5000, 3, 0, 64, 1200], 16, 2, Hkv, D, dtype, seed=40, spare=900)
+    pool = _native.KvselPages(2, c.P, 16, Hkv, D, 0 if dtype == BF16 else 1, 0, 0, c.K.data_ptr(),
+                              c.V.data_ptr())
+    lib = _native.lib()
+    n = lib.kvsel_paged_attention_bytes(ctypes.byref(pool), 5, H)
+    ws = Guarded((n,), torch.uint8)
+    flat = torch.empty(2 * 5 * H * D + 8, dtype=dtype, device=DEV)
+    q = flat[16 // flat.element_size():][:2 * 5 * H * D].view(2, 5, H, D)
+    q.copy_(normal(torch.Generator().manual_seed(41), dtype, 2, 5, H, D))
+    for fill in (0, 255):
+        ws.t.fill_(fill)
+        out, lse = a.kvsel_paged_attention(q, c.K, c.V, c.table, c.dlens, workspace=ws.t)
+        assert status() == 0 and ws.intact()
+        check_attention(c, q, out, lse)
+    with pytest.raises(a.KvselError):
+        a.kvsel_paged_attention(q, c.K, c.V, c.table, c.dlens, workspace=ws.t[:n - 1])
+    m = lib.kvsel_pages_update_bytes(ctypes.byref(pool), 7)
+    ws = Guarded((m,), torch.uint8)
+    new, parents = [5001, 5001, 4, 0, 65, 1201, 30], [0, 0, 1, 2, 3, 4, 0]
+    table, ref, free, _ = pg.update(c.table.tolist(), c.lens, parents, new, c.P, 16)
+    for fill in (0, 255):
+        ws.t.fill_(fill)
+        t, r, f = a.kvsel_pages_update(c.K, c.V, c.table, c.dlens, ints(new), parents=ints(parents),
+                                       workspace=ws.t)
+        assert status() == 0 and ws.intact()
+        assert t.tolist() == table and r.tolist() == ref and f.item() == free
+    with pytest.raises(a.KvselError):
+        a.kvsel_pages_update(c.K, c.V, c.table, c.dlens, ints(new), parents=ints(parents),
+                             workspace=ws.t[:m - 1])
+
+
 def test_calls_on_two_streams_at_once():
     """Each call has a workspace of its own: many of them in flight on two streams give what
     they give alone."""
