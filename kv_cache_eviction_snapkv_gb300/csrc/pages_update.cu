@@ -20,7 +20,7 @@
 // started pages' rows, with the whole machine: eight SMs have few instructions to spare.
 //
 // Measured: 700 sequences over 150000 pages 19 us (34 us with every entry written by the cluster,
-// 240 us by one block), four beams 9.5 us, 224 copies of started pages 41 us, 102 MB written.
+// 240 us by one block), four beams 9.5 us, 224 copies of started pages 39.5 us, 102 MB written.
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -362,7 +362,7 @@ __device__ __forceinline__ void other_entries(const PagesUpdateArgs& a, const La
 
 // Rows of started pages for their new holders, in pieces of kPiece bytes: (copy, layer, K or V,
 // piece). The copies' order does not matter: no target is a source or another's target.
-__global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__ PagesUpdateArgs a) {
+__global__ void __launch_bounds__(256, 3) pages_copy_kernel(const __grid_constant__ PagesUpdateArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Layout lo = layout_of(a.pv.num_pages, a.num_out);
   const int2 counts = *reinterpret_cast<const int2*>(a.ws + lo.count);
@@ -444,12 +444,13 @@ cudaError_t launch_pages_update(const PagesUpdateArgs& a) {
   }
   if (a.num_out == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  // as many blocks as there can be pieces or entries for, or as the SMs hold at a time (pages of
-  // one row are never started)
+  // as many blocks as there can be pieces or entries for, or some five times what the SMs hold at a
+  // time: shares of a few pieces even out (three blocks an SM 44.8 us for eight samples, eight
+  // 40.8, sixteen 39.5, one a piece 42.5). (Pages of one row are never started.)
   const int64_t pieces = ((int64_t)a.pv.row_units * kRowUnit * (a.pv.page_size - 1) + kPiece - 1) / kPiece;
   const int64_t most = std::max((int64_t)a.num_out * a.pv.layers * 2 * pieces,
                                 ((int64_t)a.num_out * a.table_width + 255) / 256);
-  cfg.gridDim = dim3((unsigned)std::min(most, 8 * (int64_t)a.sm_count));
+  cfg.gridDim = dim3((unsigned)std::min(most, 16 * (int64_t)a.sm_count));
   cfg.blockDim = dim3(256);
   cfg.stream = a.stream;
   cudaLaunchAttribute at[1];
