@@ -741,6 +741,41 @@ def test_updates_and_cuts_replay_from_a_graph():
         assert status() == a.KVSEL_ERR_SHARED_PAGE        # both go on from sequence 1: it cannot be cut
 
 
+def test_pages_beyond_four_gigabytes():
+    """Every call on the last pages of a 5 GB pool against the same call on a small one."""
+    a = api()
+    P, ps, Hkv, D = 80000, 16, 16, 128
+    gen = torch.Generator().manual_seed(50)
+    K, V = (torch.zeros((P, ps, Hkv, D), dtype=BF16, device=DEV) for _ in range(2))
+    assert K.nbytes > 4 << 30
+    far = [P - 1, P - 7, P - 3]
+    rows = [normal(gen, BF16, 3, ps, Hkv, D) for _ in range(2)]
+    K[far], V[far] = rows
+    k, v = torch.zeros((12, ps, Hkv, D), dtype=BF16, device=DEV), torch.zeros((12, ps, Hkv, D), dtype=BF16,
+                                                                               device=DEV)
+    near = [11, 5, 9]
+    k[near], v[near] = rows
+    q = normal(gen, BF16, 1, 32, D)
+    new = [normal(gen, BF16, 1, h, D) for h in (32, Hkv, Hkv)]
+    idx = torch.stack([torch.randperm(40, generator=gen)[:20] for _ in range(Hkv)], dim=1).to(torch.int32).to(DEV)
+    got = []
+    for pool, pages in (((K, V), far), ((k, v), near)):
+        table = ints([pages + [-1]])
+        r = [a.kvsel_paged_append(*new, *pool, ints([40]), table=table)]
+        r += a.kvsel_paged_attention(q, *pool, table, ints([41]))
+        r.append(a.kvsel_paged_compact(*pool, table, ints([40]), idx, ints([0, 20]), 20))
+        r += [x[pages].clone() for x in pool]
+        t, ref, free = a.kvsel_pages_update(*pool, table, ints([20]), ints([21, 21]), parents=ints([0, 0]))
+        assert status() == 0
+        assert t.tolist() == [pages[:2] + [-1, -1], [pages[0], 0, -1, -1]]
+        assert free.item() == pool[0].shape[0] - 3
+        r += [x[0, :4].clone() for x in pool]          # the copied rows
+        got.append(r)
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert bool(got[0][-1].any())
+
+
 def test_binding_checks():
     a = api()
     c = Cache([20], 16, 2, 2, 64, BF16, seed=1)
